@@ -15,8 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkivi.so")
 LIB_DEBUG = os.path.join(PKG, "libkivi_debug.so")   # -DKIVI_DEBUG: device-side bounds checks
-SOURCES = ["kivi_api.cu", "quantize.cu", "decode.cu", "noalloc.cu"]
-HEADERS = ["common.cuh", "kernels.h", "quant_rules.cuh"]
+SOURCES = ["kivi_api.cu", "quantize.cu", "decode.cu", "noalloc.cu", "paged_api.cu", "tables.cu", "rotary.cu", "append.cu",
+           "attend.cu"]
+HEADERS = ["common.cuh", "kernels.h", "quant_rules.cuh", "quant_tiles.cuh", "paged.h"]
 
 
 def nvcc() -> str:

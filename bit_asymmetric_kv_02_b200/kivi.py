@@ -47,6 +47,38 @@ class kivi_cache(ctypes.Structure):
                 ("n_quant", ctypes.c_int32), ("n_res", ctypes.c_int32)]
 
 
+class kivi_rotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class kivi_heads(ctypes.Structure):
+    _fields_ = [("x_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p), ("weight_dev", ctypes.c_void_p),
+                ("num_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)] + \
+               [(n, ctypes.c_int64) for n in ("x_batch", "x_token", "x_head", "y_batch", "y_token", "y_head")]
+
+
+class kivi_paged_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_pages", "num_seqs", "max_blocks", "num_kv_heads", "head_dim", "bits", "group_k", "group_v",
+                 "residual")]
+
+
+PAGED_BUFFERS = BUFFERS + ("block_table", "free_pages", "queue")
+
+
+class kivi_paged_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in PAGED_BUFFERS]
+
+
+class kivi_paged_plan(ctypes.Structure):
+    _fields_ = [("cu_tokens", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("runs", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("max_tokens", ctypes.c_int32), ("max_runs", ctypes.c_int32)]
+
+
+DTYPE_F16, DTYPE_BF16 = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
 _lib = None
 
 
@@ -59,7 +91,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"CUDA library not built: {path} (run python -m bit_asymmetric_kv_02_b200.build)")
     lib = ctypes.CDLL(path)
     P, I32, U64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
+    I64, F32, F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     cfgp, cachep = ctypes.POINTER(kivi_config), ctypes.POINTER(kivi_cache)
+    pcfgp, pcachep, planp = (ctypes.POINTER(s) for s in (kivi_paged_config, kivi_paged_cache, kivi_paged_plan))
+    rotp, headsp = ctypes.POINTER(kivi_rotary), ctypes.POINTER(kivi_heads)
     sig = {
         "kivi_abi_version": (I32, []),
         "kivi_strerror": (ctypes.c_char_p, [I32]),
@@ -74,6 +109,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kivi_append_decode_attention": (I32, [cfgp, cachep, P, P, P, I32, ctypes.c_float, P, P, SZ, P, P]),
         "kivi_decode_step": (I32, [cfgp, cachep, P, P, P, I32, ctypes.c_float, P, P, SZ, P, P]),
         "kivi_decode_attention_noalloc": (I32, [cfgp, cachep, P, I32, ctypes.c_float, P, P, P]),
+        "kivi_window_workspace_bytes": (SZ, [cfgp, I32]),
+        "kivi_decode_attention_window": (I32, [cfgp, cachep, P, I32, F32, I32, I32, P, P, SZ, P, P]),
+        "kivi_rotary_init": (I32, [rotp, I32, I32, F64, I32, F64, F64, F64, I32]),
+        "kivi_rotary_apply": (I32, [rotp, I32, I32, I32, P, I32, headsp, headsp, headsp, F32, P]),
+        "kivi_paged_check_config": (I32, [pcfgp]),
+        "kivi_paged_sizes": (I32, [pcfgp, ctypes.POINTER(SZ)]),
+        "kivi_paged_build_tables": (I32, [pcfgp, pcachep, I32, P, P, P, P, planp, P, P]),
+        "kivi_paged_append": (I32, [pcfgp, pcachep, planp, P, P, I64, I64, P, P]),
+        "kivi_paged_workspace_bytes": (SZ, [pcfgp, I32]),
+        "kivi_paged_decode_attention": (I32, [pcfgp, pcachep, I32, P, P, P, I32, I32, F32, I32, I32, P, P, SZ, P, P]),
         "kivi_read_status": (I32, [P, P]),
         "kivi_debug_inject": (I32, [I32, U64]),
         "kivi_debug_status": (I32, []),
@@ -165,6 +210,69 @@ def kivi_decode_attention_noalloc(cfg, cache, q_ptr: int, num_q_heads: int, scal
            "kivi_decode_attention_noalloc")
 
 
+def kivi_window_workspace_bytes(cfg, num_q_heads: int) -> int:
+    return load_library().kivi_window_workspace_bytes(ctypes.byref(cfg), num_q_heads)
+
+
+def kivi_decode_attention_window(cfg, cache, q_ptr: int, num_q_heads: int, scale: float, window: int, sinks: int,
+                                 out_ptr: int, ws_ptr: int, ws_bytes: int, status_ptr: int | None, stream: int) -> None:
+    _check(load_library().kivi_decode_attention_window(ctypes.byref(cfg), ctypes.byref(cache), q_ptr, num_q_heads,
+                                                       scale, window, sinks, out_ptr, ws_ptr, ws_bytes, status_ptr,
+                                                       stream), "kivi_decode_attention_window")
+
+
+def kivi_rotary_init(rotary_dim: int, interleaved: int, theta: float, scaling: int, factor: float, low: float,
+                     high: float, original_positions: int) -> kivi_rotary:
+    r = kivi_rotary()
+    _check(load_library().kivi_rotary_init(ctypes.byref(r), rotary_dim, interleaved, theta, scaling, factor, low, high,
+                                           original_positions), "kivi_rotary_init")
+    return r
+
+
+def kivi_rotary_apply(rotary, dtype: int, batch: int, tokens: int, positions_ptr: int | None, position0: int, q, k, v,
+                      eps: float, stream: int) -> None:
+    """q, k, v: kivi_heads or None."""
+    ref = [None if h is None else ctypes.byref(h) for h in (q, k, v)]
+    _check(load_library().kivi_rotary_apply(ctypes.byref(rotary), dtype, batch, tokens, positions_ptr, position0, *ref,
+                                            eps, stream), "kivi_rotary_apply")
+
+
+def kivi_paged_check_config(cfg: kivi_paged_config) -> int:
+    return load_library().kivi_paged_check_config(ctypes.byref(cfg))
+
+
+def kivi_paged_sizes(cfg: kivi_paged_config) -> list[int]:
+    out = (ctypes.c_size_t * len(PAGED_BUFFERS))()
+    _check(load_library().kivi_paged_sizes(ctypes.byref(cfg), out), "kivi_paged_sizes")
+    return list(out)
+
+
+def kivi_paged_build_tables(cfg, cache, num_rows: int, lens_ptr: int, new_tokens_ptr: int, lens_out_ptr: int,
+                            queue_out_ptr: int, plan, status_ptr: int | None, stream: int) -> None:
+    _check(load_library().kivi_paged_build_tables(ctypes.byref(cfg), ctypes.byref(cache), num_rows, lens_ptr,
+                                                  new_tokens_ptr, lens_out_ptr, queue_out_ptr, ctypes.byref(plan),
+                                                  status_ptr, stream), "kivi_paged_build_tables")
+
+
+def kivi_paged_append(cfg, cache, plan, k_ptr: int, v_ptr: int, token_stride: int, head_stride: int,
+                      status_ptr: int | None, stream: int) -> None:
+    _check(load_library().kivi_paged_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(plan), k_ptr, v_ptr,
+                                            token_stride, head_stride, status_ptr, stream), "kivi_paged_append")
+
+
+def kivi_paged_workspace_bytes(cfg, num_q_heads: int) -> int:
+    return load_library().kivi_paged_workspace_bytes(ctypes.byref(cfg), num_q_heads)
+
+
+def kivi_paged_decode_attention(cfg, cache, num_rows: int, lens_ptr: int, cu_tokens_ptr: int | None, q_ptr: int,
+                                num_q_rows: int, num_q_heads: int, scale: float, window: int, sinks: int, out_ptr: int,
+                                ws_ptr: int, ws_bytes: int, status_ptr: int | None, stream: int) -> None:
+    _check(load_library().kivi_paged_decode_attention(ctypes.byref(cfg), ctypes.byref(cache), num_rows, lens_ptr,
+                                                      cu_tokens_ptr, q_ptr, num_q_rows, num_q_heads, scale, window,
+                                                      sinks, out_ptr, ws_ptr, ws_bytes, status_ptr, stream),
+           "kivi_paged_decode_attention")
+
+
 def kivi_read_status(status_ptr: int, stream: int) -> int:
     return load_library().kivi_read_status(status_ptr, stream)
 
@@ -212,6 +320,7 @@ class KiviCache:
         off = (-self.workspace.data_ptr()) % 256
         self.ws_ptr = self.workspace.data_ptr() + off
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._window_ws = {}
 
     # views of the buffers in the layout of include/kivi.h
     def view(self, name: str):
@@ -292,6 +401,346 @@ class KiviCache:
                          out.data_ptr(), self.ws_ptr, self.ws_bytes, self.status.data_ptr() if status else None,
                          self._stream(stream))
         return out
+
+    def attend_window(self, q, window: int, sinks: int = 0, out=None, scale: float | None = None, stream=None,
+                      status: bool = True):
+        """attend(q) in which the newest token sees only the last `window` tokens (0: all) and the first
+        `sinks` (kivi_decode_attention_window).  The workspace for a number of query heads is allocated
+        and cleared on its first call, on the current stream: make that call before a capture."""
+        _expect(self, "q", q, (self.cfg.batch, None, self.cfg.head_dim), self.torch.float16)
+        hq = q.shape[1]
+        if hq not in self._window_ws:
+            nbytes = kivi_window_workspace_bytes(self.cfg, hq)
+            if nbytes == 0:
+                raise KiviError(1, "kivi_window_workspace_bytes")
+            self._window_ws[hq] = _Workspace(self, nbytes, stream)
+        ws = self._window_ws[hq]
+        out = _output(self, out, q, stream)
+        scale = 1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale
+        with self.torch.cuda.device(self.device):
+            kivi_decode_attention_window(self.cfg, self.c, q.data_ptr(), hq, scale, _int32("window", window),
+                                         _int32("sinks", sinks), out.data_ptr(),
+                                         ws.ptr, ws.nbytes, self.status.data_ptr() if status else None,
+                                         self._stream(stream))
+        return out
+
+    def step_rotary(self, rotary: "Rotary", k_new, v_new, q, q_weight=None, k_weight=None, eps: float = 1e-6, out=None,
+                    scale: float | None = None, stream=None, status: bool = True):
+        """step() with keys and queries as the projections give them: each head normed where it has a
+        weight and rotated to the new token's position (Rotary.apply), then appended and attended.
+        k_new, v_new, q: fp16 or bf16 [B][heads][128]."""
+        v = None if v_new.dtype == self.torch.float16 else v_new.unsqueeze(2)
+        q, k_new, v = rotary.apply(q.unsqueeze(2), k_new.unsqueeze(2), v, positions=self.n_quant + self.n_res,
+                                   q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
+        q, k_new, v_new = q.squeeze(2), k_new.squeeze(2), v_new if v is None else v.squeeze(2)
+        return self.step(k_new, v_new, q, out=out, scale=scale, stream=stream, status=status)
+
+    def read_status(self, stream=None) -> int:
+        return kivi_read_status(self.status.data_ptr(), self._stream(stream))
+
+
+# ---- argument checks and buffers of the torch layer ----------------------------------------------
+def _expect(owner, name: str, t, shape, dtype, contiguous: bool = True) -> None:
+    """Raises ValueError unless t is a tensor of that dtype and shape (None: any extent) on the owner's
+    device, dense unless contiguous is False."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != g for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: want {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or (owner.device.index is not None and t.device.index != owner.device.index):
+        raise ValueError(f"{name}: on {t.device}, the cache is on {owner.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+
+
+def _int32(name: str, x: int) -> int:
+    """x, which the C call takes as an int32 (ctypes would drop its upper bits)."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} is not an int32")
+    return x
+
+
+def _output(owner, out, q, stream):
+    """`out`, checked, or a new tensor like q that belongs to the stream the call runs on."""
+    if out is not None:
+        _expect(owner, "out", out, q.shape, owner.torch.float16)
+        return out
+    if stream is None:
+        return owner.torch.empty_like(q)
+    with owner.torch.cuda.stream(stream):
+        return owner.torch.empty_like(q)
+
+
+class _Workspace:
+    """A zeroed, 256-byte aligned workspace of its own, cleared on the stream that first uses it."""
+
+    def __init__(self, owner, nbytes: int, stream=None):
+        torch = owner.torch
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first call with a number of query heads allocates its workspace: make it before the capture")
+        if stream is None:
+            self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=owner.device)
+        else:
+            with torch.cuda.stream(stream):
+                self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=owner.device)
+        self.ptr = self.buffer.data_ptr() + (-self.buffer.data_ptr()) % 256
+        self.nbytes = nbytes
+
+
+# ---- rotary positions and head norms -------------------------------------------------------------
+class Rotary:
+    """A position rotation with optional norms per head (kivi_rotary_init, kivi_rotary_apply).
+
+    rotary_dim: leading channels of a head that rotate (a multiple of 16); interleaved: pairs (2 i, 2 i + 1)
+    instead of (i, i + rotary_dim / 2); scaling: one of ROPE_SCALINGS with its factor and, for "bands" and
+    "ramp", the turns low and high over original_positions (defaults: bands 1 and 4, ramp 1 and 32)."""
+
+    def __init__(self, rotary_dim: int = 128, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, low: float = 1.0, high: float | None = None, original_positions: int = 8192):
+        import torch
+        self.torch = torch
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling: one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+        if high is None:
+            high = 32.0 if scaling == "ramp" else 4.0
+        self.c = kivi_rotary_init(rotary_dim, 1 if interleaved else 0, theta, ROPE_SCALINGS[scaling], factor, low, high,
+                                  original_positions)
+
+    def _heads(self, name: str, x, y, weight, like, stream):
+        """kivi_heads of x ([tokens][heads][128], or [B][heads][T][128] as the cache's prefill takes it)
+        and the output tensor."""
+        torch = self.torch
+        if x.dtype != like.dtype or x.device != like.device or x.dim() != like.dim() or x.shape[-1] != 128:
+            raise ValueError(f"{name}: {x.dtype} {list(x.shape)} on {x.device} does not go with "
+                             f"{like.dtype} {list(like.shape)} on {like.device}")
+        four = x.dim() == 4
+        rows = (x.shape[0], x.shape[2]) if four else x.shape[:1]
+        if rows != ((like.shape[0], like.shape[2]) if four else like.shape[:1]):
+            raise ValueError(f"{name}: {list(x.shape)} has other tokens than {list(like.shape)}")
+        if y is None:
+            if stream is None:
+                y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
+            else:
+                with torch.cuda.stream(stream):
+                    y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
+        elif y.dtype != torch.float16 or y.shape != x.shape or y.device != x.device:
+            raise ValueError(f"{name} output: want float16 {list(x.shape)} on {x.device}")
+        sx, sy = x.stride(), y.stride()
+        if sx[-1] != 1 or sy[-1] != 1:
+            raise ValueError(f"{name}: channels must be contiguous")
+        if any(n > 1 and s == 0 for n, s in zip(y.shape, sy)):
+            raise ValueError(f"{name} output: expanded dimensions share memory")
+        if weight is not None and (weight.dtype != x.dtype or weight.shape != (128,) or weight.device != x.device
+                                   or not weight.is_contiguous()):
+            raise ValueError(f"{name} weight: want contiguous {x.dtype} [128] on {x.device}")
+        w = None if weight is None else weight.data_ptr()
+        if four:
+            b, h, t = 0, 1, 2
+            st = (sx[b], sx[t], sx[h], sy[b], sy[t], sy[h])
+        else:
+            st = (0, sx[0], sx[1], 0, sy[0], sy[1])
+        return kivi_heads(x.data_ptr(), y.data_ptr(), w, x.shape[1], 0, *st), y
+
+    def apply(self, q, k, v=None, positions=0, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
+              v_out=None, stream=None):
+        """Norms (where a weight is given) and rotates q and k, converts v, all to fp16, in one launch;
+        returns (q, k, v), v None when it was not given.  Tensors are fp16 or bf16 [tokens][heads][128] or
+        [B][heads][T][128], of any strides that keep head rows whole (slices of a fused projection).
+        positions: int32 device tensor of one entry per token ([tokens] or [B][T]), or the first position.
+        Outputs may be given; an fp16 input may be its own output."""
+        torch = self.torch
+        dtypes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
+        if q.dtype not in dtypes or not q.is_cuda or q.dim() not in (3, 4):
+            raise ValueError(f"q: want fp16 or bf16 [tokens][heads][128] or [B][heads][T][128] on the GPU, "
+                             f"got {q.dtype} {list(q.shape)} on {q.device}")
+        hq, q_out = self._heads("q", q, q_out, q_weight, q, stream)
+        hk, k_out = self._heads("k", k, k_out, k_weight, q, stream)
+        hv = None
+        if v is not None:
+            hv, v_out = self._heads("v", v, v_out, None, q, stream)
+        batch, tokens = (q.shape[0], q.shape[2]) if q.dim() == 4 else (1, q.shape[0])
+        if isinstance(positions, int):
+            ptr, first = None, _int32("positions", positions)
+        else:
+            if positions.dtype != torch.int32 or positions.numel() != batch * tokens or not positions.is_contiguous() \
+                    or positions.device != q.device:
+                raise ValueError(f"positions: want contiguous int32 of {batch * tokens} entries on {q.device}")
+            ptr, first = positions.data_ptr(), 0
+        if batch * tokens == 0:
+            return q_out, k_out, v_out
+        s = stream if stream is not None else torch.cuda.current_stream(q.device)
+        if q.device.index != torch.cuda.current_device():
+            with torch.cuda.device(q.device):
+                kivi_rotary_apply(self.c, dtypes[q.dtype], batch, tokens, ptr, first, hq, hk, hv, eps, s.cuda_stream)
+        else:
+            kivi_rotary_apply(self.c, dtypes[q.dtype], batch, tokens, ptr, first, hq, hk, hv, eps, s.cuda_stream)
+        return q_out, k_out, v_out
+
+
+# ---- torch-owned paged cache ---------------------------------------------------------------------
+class PagedPlan:
+    """One step's tables (kivi_paged_plan): cu_tokens [num_seqs + 1], positions [max_tokens], runs
+    [max_runs][8] and counts [2] as int32 tensors."""
+
+    def __init__(self, cache: "PagedKiviCache", max_tokens: int):
+        torch = cache.torch
+        runs = 2 * cache.cfg.num_seqs + max_tokens // cache.cfg.residual
+        if max_tokens < 1 or runs >= 1 << 31:
+            raise ValueError(f"max_tokens: {max_tokens}")
+        self.cu_tokens = torch.zeros(cache.cfg.num_seqs + 1, dtype=torch.int32, device=cache.device)
+        self.positions = torch.zeros(max_tokens, dtype=torch.int32, device=cache.device)
+        self.runs = torch.zeros(runs, 8, dtype=torch.int32, device=cache.device)
+        self.counts = torch.zeros(2, dtype=torch.int32, device=cache.device)
+        self.max_tokens = max_tokens
+        self.c = kivi_paged_plan(self.cu_tokens.data_ptr(), self.positions.data_ptr(), self.runs.data_ptr(),
+                                 self.counts.data_ptr(), max_tokens, runs)
+
+
+class PagedKiviCache:
+    """Caller-owned device buffers of a paged cache (include/kivi.h) as torch tensors, for sequences of
+    different lengths that come and go.  A step:
+
+        plan = cache.new_plan(max_tokens)                    # once
+        cache.build_tables(plan, lens, new_tokens)           # tables, positions, slot map; lens advanced
+        q, k, v = rotary.apply(q, k, v, positions=plan.positions[:tokens])
+        cache.append(plan, k, v)
+        out = cache.attend(lens, q, plan=plan)               # the newest token of every sequence
+
+    or all four as step().  Everything a step reads or advances is on the device, so it can be captured in a CUDA graph
+    and replayed (make one uncaptured attend() with its number of query heads first).  Calls of one cache
+    that overlap on the GPU are not allowed: they share buffers and workspaces."""
+
+    def __init__(self, num_pages: int, num_seqs: int, max_blocks: int, num_kv_heads: int, bits: int = 2, group_k: int = 32,
+                 group_v: int = 32, residual: int = 128, head_dim: int = 128, num_q_heads: int | None = None, device=None):
+        import torch
+        self.torch = torch
+        self.device = torch.device(device or "cuda")
+        self.cfg = kivi_paged_config(num_pages, num_seqs, max_blocks, num_kv_heads, head_dim, bits, group_k, group_v,
+                                     residual)
+        st = kivi_paged_check_config(self.cfg)
+        if st != KIVI_OK:
+            raise KiviError(st, "kivi_paged_check_config")
+        self.buffers = {}
+        for name, nbytes in zip(PAGED_BUFFERS, kivi_paged_sizes(self.cfg)):
+            self.buffers[name] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
+        self.device = self.buffers["queue"].device
+        self.c = kivi_paged_cache(*[self.buffers[n].data_ptr() for n in PAGED_BUFFERS])
+        self.view("block_table").fill_(-1)
+        self.view("free_pages").copy_(torch.arange(num_pages, dtype=torch.int32))
+        self.view("queue").copy_(torch.tensor([0, num_pages]))
+        self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._ws = {}
+        if num_q_heads is not None:
+            self._workspace(num_q_heads, None)
+
+    def _workspace(self, num_q_heads: int, stream) -> _Workspace:
+        ws = self._ws.get(num_q_heads)
+        if ws is None:
+            nbytes = kivi_paged_workspace_bytes(self.cfg, num_q_heads)
+            if nbytes == 0:
+                raise KiviError(1, "kivi_paged_workspace_bytes")
+            ws = self._ws[num_q_heads] = _Workspace(self, nbytes, stream)
+        return ws
+
+    def _stream(self, stream) -> int:
+        return (stream if stream is not None else self.torch.cuda.current_stream(self.device)).cuda_stream
+
+    def _call(self, fn, *args) -> None:
+        if self.device.index != self.torch.cuda.current_device():
+            with self.torch.cuda.device(self.device):
+                fn(self.cfg, self.c, *args)
+        else:
+            fn(self.cfg, self.c, *args)
+
+    def view(self, name: str):
+        """The buffer in the layout of include/kivi.h."""
+        t, c = self.torch, self.cfg
+        N, S, H, R, d, P = c.num_pages, c.num_seqs, c.num_kv_heads, c.residual, c.head_dim, 32 // c.bits
+        dtype, shape = {
+            "k_codes": (t.int32, (N, H, R, d // P)), "v_codes": (t.int32, (N, H, R // P, d)),
+            "k_scale": (t.float16, (N, H, d // c.group_k)), "k_zero": (t.float16, (N, H, d // c.group_k)),
+            "v_scale": (t.float16, (N, H, R // c.group_v)), "v_zero": (t.float16, (N, H, R // c.group_v)),
+            "k_res": (t.float16, (S, H, R, d)), "v_res": (t.float16, (S, H, R, d)),
+            "block_table": (t.int32, (S, c.max_blocks)), "free_pages": (t.int32, (N,)), "queue": (t.int64, (2,)),
+        }[name]
+        n = math.prod(shape) * dtype.itemsize
+        return self.buffers[name][:n].view(dtype).view(shape)
+
+    def new_plan(self, max_tokens: int) -> PagedPlan:
+        """Buffers for steps of at most max_tokens new tokens."""
+        return PagedPlan(self, max_tokens)
+
+    def build_tables(self, plan: PagedPlan, lens, new_tokens, lens_out=None, queue_out=None, stream=None,
+                     status: bool = True) -> None:
+        """Tables of a step (kivi_paged_build_tables): lens, new_tokens int32 [n], n <= num_seqs.  The new
+        lengths and queue replace the old ones unless lens_out (int32 [n]) or queue_out (int64 [2]) take them."""
+        i32 = self.torch.int32
+        _expect(self, "lens", lens, (None,), i32)
+        _expect(self, "new_tokens", new_tokens, lens.shape, i32)
+        if lens_out is not None:
+            _expect(self, "lens_out", lens_out, lens.shape, i32)
+        if queue_out is not None:
+            _expect(self, "queue_out", queue_out, (2,), self.torch.int64)
+        self._call(kivi_paged_build_tables, lens.shape[0], lens.data_ptr(), new_tokens.data_ptr(),
+                   (lens if lens_out is None else lens_out).data_ptr(),
+                   self.c.queue if queue_out is None else queue_out.data_ptr(), plan.c,
+                   self.status.data_ptr() if status else None, self._stream(stream))
+
+    def append(self, plan: PagedPlan, k, v, stream=None, status: bool = True) -> None:
+        """Writes a step's tokens (kivi_paged_append): k, v fp16 [tokens][H][128] of equal strides that keep
+        head rows whole, tokens at least the plan's count."""
+        shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
+        _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
+        _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
+        sk = k.stride()
+        if sk[2] != 1 or sk != v.stride():
+            raise ValueError(f"k, v: strides {sk} and {v.stride()}; want equal strides and contiguous channels")
+        if k.shape[0] == 0:
+            return
+        c = plan.c
+        if k.shape[0] < plan.max_tokens:  # a plan of more tokens than there are rows must not read past them
+            c = kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, k.shape[0], c.max_runs)
+        self._call(kivi_paged_append, c, k.data_ptr(), v.data_ptr(), sk[0], sk[1],
+                   self.status.data_ptr() if status else None, self._stream(stream))
+
+    def attend(self, lens, q, plan: PagedPlan | None = None, out=None, scale: float | None = None, window: int = 0,
+               sinks: int = 0, stream=None, status: bool = True):
+        """Attention of the newest token of each sequence (kivi_paged_decode_attention): lens int32 [n], q
+        fp16 [rows][Hq][128].  Without a plan row i is sequence i; with one, q holds a row per new token of
+        the step and only the last of each sequence is attended (other rows of out stay as they are, so
+        give `out` or do not read them)."""
+        _expect(self, "lens", lens, (None,), self.torch.int32)
+        _expect(self, "q", q, (None, None, self.cfg.head_dim), self.torch.float16)
+        if plan is None and q.shape[0] < lens.shape[0]:
+            raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
+        ws = self._workspace(q.shape[1], stream)
+        out = _output(self, out, q, stream)
+        if q.shape[0] == 0:
+            return out
+        self._call(kivi_paged_decode_attention, lens.shape[0], lens.data_ptr(),
+                   None if plan is None else plan.c.cu_tokens, q.data_ptr(), q.shape[0], q.shape[1],
+                   1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
+                   _int32("sinks", sinks), out.data_ptr(), ws.ptr,
+                   ws.nbytes, self.status.data_ptr() if status else None, self._stream(stream))
+        return out
+
+    def step(self, plan: PagedPlan, lens, new_tokens, q, k, v, rotary: Rotary | None = None, q_weight=None, k_weight=None,
+             eps: float = 1e-6, out=None, scale: float | None = None, window: int = 0, sinks: int = 0, stream=None,
+             status: bool = True):
+        """A step of a layer: tables, norms and rotation (with a rotary), append, attention; lens advances.
+        q, k, v: [tokens][heads][128], fp16 (with a rotary: or bf16), packed by sequence; new_tokens sums to
+        their rows or fewer.  Returns the attention output [tokens][Hq][128] (rows: see attend)."""
+        if q.shape[0] > plan.max_tokens:
+            raise ValueError(f"q: {q.shape[0]} rows, the plan holds {plan.max_tokens}")
+        self.build_tables(plan, lens, new_tokens, stream=stream, status=status)
+        if rotary is not None:
+            q, k, v16 = rotary.apply(q, k, v if v.dtype != self.torch.float16 else None,
+                                     positions=plan.positions[:q.shape[0]], q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                     stream=stream)
+            v = v if v16 is None else v16
+        if k.stride() != v.stride():
+            k, v = k.contiguous(), v.contiguous()
+        self.append(plan, k, v, stream=stream, status=status)
+        return self.attend(lens, q.contiguous(), plan=plan, out=out, scale=scale, window=window, sinks=sinks, stream=stream,
+                           status=status)
 
     def read_status(self, stream=None) -> int:
         return kivi_read_status(self.status.data_ptr(), self._stream(stream))

@@ -267,6 +267,190 @@ int kivi_decode_attention_noalloc(const kivi_config* cfg, const kivi_cache* cach
                                   int32_t num_q_heads, float scale, uint16_t* out_dev, int32_t* dev_status,
                                   void* stream);
 
+/* ---- Sliding window over the contiguous cache -------------------------------------------------- */
+
+/* Bytes of scratch workspace kivi_decode_attention_window needs for this config and query-head count
+ * (0 if the arguments are invalid).  The size does not depend on the cache counters. */
+size_t kivi_window_workspace_bytes(const kivi_config* cfg, int32_t num_q_heads);
+
+/*
+ * Decode attention with a sliding window and attention sinks: the query is the sequence's newest
+ * token, and of the T = n_quant + n_res cached tokens it sees token t iff t < sinks or
+ * t >= T - window.  Otherwise kivi_decode_attention: the same cache, layouts and workspace rules
+ * (zero before its first use, left zero, not shared by overlapping calls; 256-byte aligned).  Only
+ * blocks that hold a visible token are read; what the other tokens hold (NaN included) has no
+ * effect, except that a block which is visible in part is dequantized with its stored (s, z).
+ * window >= 0 (0: every token is visible), sinks >= 0.  Hq is any multiple of H with Hq / H <= 64.
+ * Base groups only: online_k and fine_groups give KIVI_ERR_UNSUPPORTED.  One kernel launch.
+ */
+int kivi_decode_attention_window(const kivi_config* cfg, const kivi_cache* cache, const uint16_t* q_dev,
+                                 int32_t num_q_heads, float scale, int32_t window, int32_t sinks, uint16_t* out_dev,
+                                 void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ---- Rotary positions and head norms ----------------------------------------------------------- */
+
+/* Element type of kivi_rotary_apply's inputs. */
+#define KIVI_DTYPE_F16 0
+#define KIVI_DTYPE_BF16 1
+
+/* How the rotation frequencies theta^(-2 i / rotary_dim) are scaled for long contexts. */
+#define KIVI_ROPE_NONE 0
+#define KIVI_ROPE_LINEAR 1 /* every frequency divided by `factor` (positions interpolated) */
+#define KIVI_ROPE_BASE 2   /* theta multiplied by factor^(rotary_dim / (rotary_dim - 2)) */
+#define KIVI_ROPE_BANDS 3  /* by turns over the original context: frequencies with at least `high` turns
+                              kept, with at most `low` divided by `factor`, linear in the turns between */
+#define KIVI_ROPE_RAMP 4   /* the same idea linear in the pair index, between the pairs that make `high`
+                              and `low` turns; cos and sin also times 0.1 ln(factor) + 1 */
+
+/*
+ * A rotation: filled by kivi_rotary_init on the host and read by kivi_rotary_apply (plain data, no
+ * pointers).  turns[i] is pair i's frequency in turns per position as a 64-bit fraction (2^64 = one
+ * turn), so that position * turns[i] mod 2^64 is the angle itself: far positions lose nothing.
+ */
+typedef struct kivi_rotary {
+  int32_t rotary_dim;  /* leading channels of a head that rotate: a multiple of 16, 0..128 */
+  int32_t interleaved; /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  float magnitude;     /* factor of cos and sin */
+  int32_t reserved;
+  uint64_t turns[64];
+} kivi_rotary;
+
+/* Fills *rotary.  theta > 1; factor >= 1; low, high: turns (KIVI_ROPE_BANDS, KIVI_ROPE_RAMP: 0 < low <
+ * high); original_positions >= 1 is the context length the model was trained on.  Host-only. */
+int kivi_rotary_init(kivi_rotary* rotary, int32_t rotary_dim, int32_t interleaved, double theta, int32_t scaling,
+                     double factor, double low, double high, int32_t original_positions);
+
+/*
+ * Heads of one kind (queries, keys or values) of batch x tokens rows of 128 channels.  Strides are in
+ * elements (head rows are contiguous and 16-byte aligned: every stride a multiple of 8), so any of
+ * [tokens][heads][128], [B][heads][T][128] or a slice of a fused projection's output will do.
+ */
+typedef struct kivi_heads {
+  const void* x_dev;      /* fp16 or bf16 input */
+  uint16_t* y_dev;        /* fp16 output; may be x_dev with the same strides when x is fp16 */
+  const void* weight_dev; /* norm weight [128] in the input's type; NULL: no norm */
+  int32_t num_heads;      /* 0: these heads are absent (pointers not used) */
+  int32_t reserved;
+  int64_t x_batch, x_token, x_head;
+  int64_t y_batch, y_token, y_head;
+} kivi_heads;
+
+/*
+ * Norm and rotation of queries and keys in one pass, what precedes the cache's calls: for each head row
+ *   x <- x / sqrt(mean(x^2) + eps) * weight   (where weight is given)
+ *   (a, b) <- m (a cos - b sin, a sin + b cos) for each pair, at angle position * frequency
+ * and one rounding to fp16, the type the cache holds (a value beyond fp16's range becomes infinite).
+ * Values are only converted to fp16 (v may be NULL or have no heads).  positions_dev: int32
+ * [batch][tokens], any sign; NULL: row i of every batch entry is at position position0 + i.
+ * Nothing is enqueued for batch x tokens == 0.  One kernel launch.
+ */
+int kivi_rotary_apply(const kivi_rotary* rotary, int32_t dtype, int32_t batch, int32_t tokens,
+                      const int32_t* positions_dev, int32_t position0, const kivi_heads* q, const kivi_heads* k,
+                      const kivi_heads* v, float eps, void* stream);
+
+/* ---- Paged cache: sequences of different lengths ------------------------------------------------ */
+
+/*
+ * A paged cache holds up to num_seqs sequences.  A page is one R-token block of all KV heads (codes
+ * and (s, z), the layout of a kivi_cache of batch num_pages and capacity R); every sequence has R
+ * residual rows of its own.  A sequence of L tokens uses pages block_table[seq][0 .. L / R - 1], and
+ * its newest ((L - 1) mod R) + 1 tokens are in its residual rows in fp16: the block that has just
+ * filled is in both until the next token arrives, and is attended in fp16, as kivi_decode_step does.
+ *   k_codes uint32 [num_pages][H][R][d/P]      v_codes uint32 [num_pages][H][R/P][d]
+ *   k_scale, k_zero fp16 [num_pages][H][d/G_k] v_scale, v_zero fp16 [num_pages][H][R/G_v]
+ *   k_res, v_res fp16 [num_seqs][H][R][d]      block_table int32 [num_seqs][max_blocks]
+ *   free_pages int32 [num_pages]: a ring; queue int64 {head, tail}: pages free_pages[i mod num_pages],
+ *   head <= i < tail, are free.  The caller starts it with every page (head 0, tail num_pages).
+ * Lengths live on the device (int32, one per sequence), so a captured graph of the calls below can be
+ * replayed step after step.  Rules: the group, bits and head_dim rules of kivi_config; residual in
+ * {128, 256, 512}; 1 <= num_seqs <= 8192; num_pages, max_blocks, num_kv_heads >= 1; max_blocks * R and
+ * num_seqs * H * R below 2^31.  Base groups only.
+ */
+typedef struct kivi_paged_config {
+  int32_t num_pages, num_seqs, max_blocks;
+  int32_t num_kv_heads, head_dim, bits, group_k, group_v, residual;
+} kivi_paged_config;
+
+typedef struct kivi_paged_cache {
+  uint32_t *k_codes, *v_codes;
+  uint16_t *k_scale, *k_zero, *v_scale, *v_zero;
+  uint16_t *k_res, *v_res;
+  int32_t *block_table, *free_pages;
+  int64_t* queue;
+} kivi_paged_cache;
+
+/* Index of each buffer in kivi_paged_sizes' output: KIVI_BUF_* up to KIVI_BUF_V_RES, then these. */
+enum { KIVI_BUF_BLOCK_TABLE = KIVI_NUM_BUFS, KIVI_BUF_FREE_PAGES, KIVI_BUF_QUEUE, KIVI_NUM_PAGED_BUFS };
+
+int kivi_paged_check_config(const kivi_paged_config* cfg);
+int kivi_paged_sizes(const kivi_paged_config* cfg, size_t* out_bytes);
+
+/*
+ * What kivi_paged_build_tables works out for one step, in device memory of the caller:
+ *   cu_tokens int32 [num_seqs + 1]  row of each sequence's first new token in the step's packed tensors
+ *   positions int32 [max_tokens]    position of each new token in its sequence
+ *   runs      int32 [max_runs][8]   the slot map: one entry per block that new tokens touch, by sequence
+ *     and block: {sequence, page the block completes into or -1, row of its first new token, first and
+ *     end row in the block, flags (1: the sequence's last run, whose rows stay in the residual; 2: left
+ *     to the run that chains to it), chain (runs up to the one to do next, 0: none), 0}
+ *   counts    int32 [2]             runs, new tokens
+ * max_runs >= 2 * num_seqs + max_tokens / R.
+ */
+typedef struct kivi_paged_plan {
+  int32_t *cu_tokens, *positions, *runs, *counts;
+  int32_t max_tokens, max_runs;
+} kivi_paged_plan;
+
+/*
+ * Block tables and slot map of a step, built from request lengths: sequence i < num_rows has
+ * lens_dev[i] cached tokens and gets new_tokens_dev[i] more (0: none; negative: the request is done,
+ * its pages go back to the queue's tail and its length becomes 0).  Blocks that fill get pages from
+ * the queue's head, in order of sequence and block; pages that come back in this call are handed out
+ * from the next one on.  lens_out_dev (num_rows) and queue_out_dev (2) receive the new lengths and
+ * queue; they may be lens_dev and cache->queue.  Table rows from num_rows on, entries behind a
+ * sequence's blocks, and positions and runs behind the counts are left as they are.
+ * A row that cannot be served (a length that is negative or needs more than max_blocks, no page left)
+ * reports KIVI_ERR_CAPACITY in dev_status, keeps its length, gets no run, and its tokens' positions
+ * are -1; the other rows are served.  More than max_tokens new tokens in all: KIVI_ERR_CAPACITY, and
+ * nothing is planned (counts and cu_tokens 0, lengths and queue unchanged).  One kernel launch.
+ */
+int kivi_paged_build_tables(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
+                            const int32_t* lens_dev, const int32_t* new_tokens_dev, int32_t* lens_out_dev,
+                            int64_t* queue_out_dev, const kivi_paged_plan* plan, int32_t* dev_status, void* stream);
+
+/*
+ * Writes a step's new tokens into the cache along the plan's runs: rows into the residual and, for
+ * blocks that the step completes, codes and (s, z) into their page, bit-exactly as kivi_flush_residual
+ * would.  k_dev, v_dev: fp16, new token t of head h at t * token_stride + h * head_stride (elements,
+ * multiples of 8), tokens packed in the order of cu_tokens.  A run whose sequence, page or rows lie
+ * outside the cache or max_tokens is skipped and KIVI_ERR_INTERNAL reported in dev_status.
+ * One kernel launch.
+ */
+int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
+                      const uint16_t* k_dev, const uint16_t* v_dev, int64_t token_stride, int64_t head_stride,
+                      int32_t* dev_status, void* stream);
+
+/* Bytes of scratch workspace kivi_paged_decode_attention needs (0 if the arguments are invalid). */
+size_t kivi_paged_workspace_bytes(const kivi_paged_config* cfg, int32_t num_q_heads);
+
+/*
+ * Decode attention of one query token per sequence over the paged cache:
+ *   out[i][h] = softmax(scale * q[i][h] . [D(Kq); Kres]^T) [D(Vq); Vres] over sequence i's
+ * lens_dev[i] tokens (the new one included), i < num_rows, with the window and sinks of
+ * kivi_decode_attention_window.  q_dev, out_dev: fp16 [rows][Hq][d].  cu_tokens_dev NULL: row i is
+ * sequence i.  Else (a step's cu_tokens, for batches that mix prompts and single tokens) sequence i's
+ * row is cu_tokens[i + 1] - 1, its last new token, and sequences without a new token are skipped.
+ * num_q_rows: rows of q_dev and out_dev; a row outside is skipped (KIVI_ERR_INTERNAL).
+ * A sequence of length 0 gives a row of zeros; a page outside the pool is left out and
+ * KIVI_ERR_INTERNAL reported.  The other rows of out_dev are left as they are.
+ * Workspace rules and Hq as in kivi_decode_attention_window.  One kernel launch.
+ */
+int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
+                                const int32_t* lens_dev, const int32_t* cu_tokens_dev, const uint16_t* q_dev,
+                                int32_t num_q_rows, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                                uint16_t* out_dev, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
+                                void* stream);
+
 /* Synchronizes `stream` and returns the device-side status word (KIVI_OK if it is 0). */
 int kivi_read_status(const int32_t* dev_status, void* stream);
 
