@@ -69,6 +69,8 @@ struct AttendArgs {
   int32_t* tickets;
   int32_t* status;
   int rows, heads, gqa;
+  int max_rows;          // rows the workspace is for
+  int passes, per_pass;  // query passes per KV head and queries of a pass (set by launch_attend)
   int len, quant;  // without lens: tokens of every sequence, and how many of them are codes
   int q_rows;
   int num_pages, max_blocks, blocks_per_head;
@@ -76,7 +78,10 @@ struct AttendArgs {
   int window, sinks;  // window: INT32_MAX when every token is visible
   float qscale;       // softmax scale * log2(e)
 };
-size_t attend_workspace_bytes(long long rows, int heads, int gqa);
-cudaError_t launch_attend(const AttendArgs& a, int bits, void* workspace, cudaStream_t stream);
+constexpr int kAttendResTokens = 16;  // tokens of a residual unit
+constexpr int attend_unit_tokens(int bits) { return 256 / bits; }
+// max_units: units (of codes and of residual rows) a head can have; rows * max_units below 2^31.
+size_t attend_workspace_bytes(long long rows, int heads, int gqa, long long max_units);
+cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* workspace, cudaStream_t stream);
 
 }  // namespace kivi

@@ -66,11 +66,23 @@ int check_attend(int heads, int num_q_heads, float scale, int window, int sinks,
   return KIVI_OK;
 }
 
-int run_attend(const kivi::AttendArgs& a, int bits, void* ws, size_t ws_bytes, void* stream) {
-  const size_t need = kivi::attend_workspace_bytes(a.rows, a.heads, a.gqa);
-  if (need == 0) return KIVI_ERR_CUDA;
+// 8 KB units a head of at most `blocks` R-token blocks and R residual rows is cut into.
+long long max_units(int bits, int residual, long long blocks) {
+  return blocks * (residual / kivi::attend_unit_tokens(bits)) + residual / kivi::kAttendResTokens;
+}
+
+// Workspace of max_rows rows; 0 where the rows' units are past the kernel's 32-bit prefix sums.
+size_t attend_bytes(int max_rows, int heads, int num_q_heads, long long units) {
+  if (num_q_heads < 1 || num_q_heads % heads != 0 || num_q_heads / heads > kMaxGqa || max_rows > kMaxSeqs) return 0;
+  if (max_rows * units > 0x7fffffffll) return 0;
+  return kivi::attend_workspace_bytes(max_rows, heads, num_q_heads / heads, units);
+}
+
+int run_attend(const kivi::AttendArgs& a, int bits, long long units, void* ws, size_t ws_bytes, void* stream) {
+  const size_t need = attend_bytes(a.max_rows, a.heads, a.heads * a.gqa, units);
+  if (need == 0) return KIVI_ERR_UNSUPPORTED;
   if (!aligned(ws, 256) || ws_bytes < need) return KIVI_ERR_WORKSPACE;
-  return kivi::launch_attend(a, bits, ws, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
+  return kivi::launch_attend(a, bits, units, ws, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
 }
 
 bool heads_ok(const kivi_heads* h) {
@@ -102,9 +114,8 @@ void set_heads(kivi::RotaryHeads* to, const kivi_heads* h, int rotate) {
 extern "C" {
 
 size_t kivi_window_workspace_bytes(const kivi_config* cfg, int32_t num_q_heads) {
-  if (kivi_check_config(cfg) != KIVI_OK || num_q_heads < 1 || num_q_heads % cfg->num_kv_heads != 0) return 0;
-  if (num_q_heads / cfg->num_kv_heads > kMaxGqa || cfg->batch > kMaxSeqs) return 0;
-  return kivi::attend_workspace_bytes(cfg->batch, cfg->num_kv_heads, num_q_heads / cfg->num_kv_heads);
+  if (kivi_check_config(cfg) != KIVI_OK) return 0;
+  return attend_bytes(cfg->batch, cfg->num_kv_heads, num_q_heads, max_units(cfg->bits, cfg->residual, cfg->capacity / cfg->residual));
 }
 
 int kivi_decode_attention_window(const kivi_config* cfg, const kivi_cache* cache, const uint16_t* q_dev,
@@ -134,14 +145,14 @@ int kivi_decode_attention_window(const kivi_config* cfg, const kivi_cache* cache
   a.v_zero = cache->v_zero;
   a.k_res = cache->k_res;
   a.v_res = cache->v_res;
-  a.rows = a.q_rows = cfg->batch;
+  a.rows = a.max_rows = a.q_rows = cfg->batch;
   a.len = cache->n_quant + cache->n_res;
   a.quant = cache->n_quant;
   a.blocks_per_head = cfg->capacity / R;
   a.lg_r = log2i(R);
   a.lg_gk = log2i(cfg->group_k);
   a.lg_gv = log2i(cfg->group_v);
-  return run_attend(a, cfg->bits, workspace_dev, workspace_bytes, stream);
+  return run_attend(a, cfg->bits, max_units(cfg->bits, R, a.blocks_per_head), workspace_dev, workspace_bytes, stream);
 }
 
 int kivi_rotary_init(kivi_rotary* r, int32_t rotary_dim, int32_t interleaved, double theta, int32_t scaling, double factor,
@@ -304,10 +315,8 @@ int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cach
 }
 
 size_t kivi_paged_workspace_bytes(const kivi_paged_config* cfg, int32_t num_q_heads) {
-  if (check_paged(cfg) != KIVI_OK || num_q_heads < 1 || num_q_heads % cfg->num_kv_heads != 0 ||
-      num_q_heads / cfg->num_kv_heads > kMaxGqa)
-    return 0;
-  return kivi::attend_workspace_bytes(cfg->num_seqs, cfg->num_kv_heads, num_q_heads / cfg->num_kv_heads);
+  if (check_paged(cfg) != KIVI_OK) return 0;
+  return attend_bytes(cfg->num_seqs, cfg->num_kv_heads, num_q_heads, max_units(cfg->bits, cfg->residual, cfg->max_blocks));
 }
 
 int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
@@ -336,13 +345,14 @@ int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_c
   a.lens = lens_dev;
   a.cu_tokens = cu_tokens_dev;
   a.rows = num_rows;
+  a.max_rows = cfg->num_seqs;
   a.q_rows = num_q_rows;
   a.num_pages = cfg->num_pages;
   a.max_blocks = cfg->max_blocks;
   a.lg_r = log2i(cfg->residual);
   a.lg_gk = log2i(cfg->group_k);
   a.lg_gv = log2i(cfg->group_v);
-  return run_attend(a, cfg->bits, workspace_dev, workspace_bytes, stream);
+  return run_attend(a, cfg->bits, max_units(cfg->bits, cfg->residual, cfg->max_blocks), workspace_dev, workspace_bytes, stream);
 }
 
 }  // extern "C"
