@@ -34,13 +34,13 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kResTokens = kAttendResTokens;      // tokens per residual unit
 constexpr int kHalfBytes = 4096;                  // the K or the V part of a unit
-constexpr int kKRow = 272;                        // a residual K row in shared memory (ldmatrix without conflicts)
-constexpr int kVPiece = 1024, kVPieceStride = 1040;  // V word rows 2 t and 2 t + 1, four bank groups for t = 0..3
+constexpr int kRow = 272;                         // a residual row in shared memory (ldmatrix without conflicts)
+constexpr int kVPieceStride = 1040;               // V word rows 2 t and 2 t + 1, four bank groups for t = 0..3
 constexpr int kQRow = 272;                        // a raw query row in shared memory
 constexpr int kPart = 132;                        // floats of a partial: m, l, Z, pad, o[128]
 constexpr int kMaxCtas = 160;
-constexpr uint64_t kWaitNs = 2000000000ull;       // bound of each wait for a copy
-constexpr float kNoMax = -1e38f;                  // running maximum of no token: finite, so that exp2 of it minus itself is 1
+constexpr float kNoMax = -1e38f;                  // reference of a part without tokens: finite, and below every other
+constexpr float kSlack = 4.f;                     // logits may pass the reference by this much: weights up to 2^4
 
 #ifndef KIVI_ATTEND_WARPS
 #define KIVI_ATTEND_WARPS 12
@@ -63,11 +63,32 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed, for the whole warp
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  __syncwarp();
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -78,23 +99,19 @@ __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // The codes of a word as pairs (j, j + P / 2) of fp16 subnormals: code 4^e(j) 2^-24 (16^e at 4 bits).
+// The upper pairs are taken from the word shifted down (upper_codes).
 template <int BITS>
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&a)[16 / BITS]) {
-  if constexpr (BITS == 2) {
-#pragma unroll
-    for (int j = 0; j < 5; ++j) a[j] = w & (0x00030003u << (2 * j));
-    const uint32_t w2 = w >> 10;
-#pragma unroll
-    for (int j = 5; j < 8; ++j) a[j] = w2 & (0x00030003u << (2 * (j - 5)));
-  } else {
-    const uint32_t w2 = w >> 8;
-    a[0] = w & 0x000F000Fu;
-    a[1] = w & 0x00F000F0u;
-    a[2] = w2 & 0x000F000Fu;
-    a[3] = w2 & 0x00F000F0u;
-  }
+__device__ __forceinline__ uint32_t upper_codes(uint32_t w) {
+  return w >> (BITS == 2 ? 10 : 8);
 }
-// log2 of the factor code_pairs leaves on pair j.
+template <int BITS>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t upper, int j) {
+  if constexpr (BITS == 2)
+    return j < 5 ? w & (0x00030003u << (2 * j)) : upper & (0x00030003u << (2 * (j - 5)));
+  else
+    return (j < 2 ? w : upper) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+// log2 of the factor code_pair leaves on pair j.
 template <int BITS>
 __device__ __forceinline__ constexpr int pair_shift(int j) {
   return BITS == 2 ? 2 * (j < 5 ? j : j - 5) : 4 * (j & 1);
@@ -161,14 +178,82 @@ __device__ __forceinline__ int q_row(const AttendArgs& a, int b, bool* bad) {
   return row;
 }
 
+// Units per head of row i (0: it takes no query).
+template <int UT>
+__device__ __forceinline__ int row_units(const AttendArgs& a, int i) {
+  bool bad = false;
+  return q_row(a, i, &bad) < 0 ? 0 : units_of<UT>(span_of(a, i, &bad)).total;
+}
+
+// Where a warp is: the unit it fetched last (seq, head and pass he, index local of the head's units), and the span of
+// the head it works on, one unit behind.
+struct Cursor {
+  int seq, he, local;
+  Units un;
+  Span sp, now;
+  int he_now, seq_now;
+};
+
+// The cursor at unit `local` of a head, for the whole warp: {index, plain successors, block or its base, 1: residual + 2: ok}.
+template <int UT>
+__device__ __noinline__ int4 enter(const AttendArgs& a, Cursor& c, int seq, int he, int local, bool new_seq) {
+  Units un;
+  Span sp;
+  if (new_seq) {
+    bool bad;
+    sp = span_of(a, seq, &bad);
+    un = units_of<UT>(sp);
+  } else {
+    sp = c.sp;
+    un = c.un;
+  }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    c.seq = seq;
+    c.he = he;
+    c.local = local;
+    c.sp = sp;
+    c.un = un;
+  }
+  __syncwarp();
+  const int h = he / a.passes;
+  const bool res = local >= un.q_units;
+  const int r = res ? local - un.q_units : local, sink = res ? un.r_sink : un.q_sink, gap = res ? un.r_gap : un.q_gap;
+  const int end = res ? un.total - un.q_units : un.q_units, x = r + (r >= sink ? gap : 0);
+  int4 out = make_int4(x, (r < sink ? sink : end) - r - 1, h, 2);
+  if (res)  // not ok: the one unit of a row without tokens
+    out.z = seq * a.heads + h, out.w = 1 + (x * kResTokens < sp.len - sp.quant ? 2 : 0);
+  else if (a.block_table == nullptr)
+    out.z = static_cast<int>((static_cast<uint32_t>(seq) * a.heads + h) * a.blocks_per_head);
+  return out;
+}
+// The unit behind the last of a run of plain successors.
+template <int UT>
+__device__ __noinline__ int4 next_run(const AttendArgs& a, Cursor& c, int steps) {
+  int seq = c.seq, he = c.he, local = c.local + steps;
+  bool new_seq = false;
+  if (local >= c.un.total) {
+    local = 0;
+    if (++he == a.heads * a.passes) {
+      he = 0;
+      new_seq = true;
+      do ++seq;
+      while (seq < a.rows - 1 && row_units<UT>(a, seq) == 0);
+    }
+  }
+  return enter<UT>(a, c, seq, he, local, new_seq);
+}
+
 template <int BITS, int NB>
 struct __align__(128) WarpSmem {
-  uint8_t k[kResTokens * kKRow];
-  uint8_t v[4 * kVPieceStride];
+  uint8_t k[kResTokens * kRow];
+  uint8_t v[kResTokens * kRow];
   uint4 p[NB][BITS == 2 ? 128 : 64];  // P operands: column, code pair and word rows (p_slot)
+  uint4 qh[NB][4][32];                // each lane's share of the K product's B operand, before s
   uint8_t q[NB][4 * kQRow];           // the head's raw queries
-  uint64_t bar[2];
+  Cursor cur;
 };
+static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes, "a buffer holds either kind of half");
 
 template <int BITS, int NB>
 struct Attender {
@@ -183,135 +268,121 @@ struct Attender {
 
   const AttendArgs& a;
   Smem& S;
-  const int* cum;  // [rows + 1] units per head before each row
   const int lane, g, t;
-  const int he_count;  // (KV head, pass) pairs per row
   long long worker, workers, total;
 
-  // a unit: where its halves are, and which of its tokens are visible
-  struct Unit {
-    long long off;           // bytes from the start of the K and V arrays
-    long long ks, vs;        // first (s, z) of the block
-    int tok0, start, sink_end, len;
-    bool ok, res, full;
-  };
-  // the position of the unit that is fetched next
-  int seq, he, local;
-  Units un;
-  Span sp;
+  // the unit fetched last: its index among the row's units of codes or residual rows, how many plain successors it has,
+  // whether it can be read, and where it is
+  int x, run_, steps_;  // steps_: since the cursor was written
+  bool res, ok;
+  uint32_t blk, hbase;    // block; KV head (pages) or first block of the head (contiguous)
+  long long off;          // bytes from the start of the K and V arrays
+  const int32_t* table;   // the row's block table, or null
+  int full_from, sink_full;  // units from the one and below the other are visible whole
 
-  // state of the head in hand: lane (g, t) is query t (of each column block) and channels 16 g .. 16 g + 15
-  uint32_t qh[NB][16];  // B-operand share of lane (column g, t): channels 32 t .. 32 t + 31 of query g / 2, scaled
-  float m[NB], l[NB], Z[NB], o[NB][8][4];
+  // state of the head in hand: lane (g, t) is query t (of each column block) and channels 16 g .. 16 g + 15.
+  // Weights are 2^(logit - m): m is the largest logit when it was last raised, by at most kSlack below the largest.
+  float m[NB], thr[NB], l[NB], Z[NB], o[NB][8][4];
   float qs[NB][4];   // scale * log2 e * sum of q over channels 32 i .. 32 i + 31
   int qe[NB];        // exponent of the largest |q|
-  int eref;          // exponent field of the largest V scale so far: o carries 2^(28 - eref - 24)
-  uint32_t kphase, vphase;
+  int eref;          // exponent field of the largest V scale so far: o carries 2^-eref (P operands 2^(24 - eref))
 
-  __device__ Attender(const AttendArgs& args, Smem& smem, const int* c, int ln)
-      : a(args), S(smem), cum(c), lane(ln), g(ln >> 2), t(ln & 3), he_count(args.heads * args.passes), kphase(0), vphase(0) {}
+  __device__ Attender(const AttendArgs& args, Smem& smem, int ln) : a(args), S(smem), lane(ln), g(ln >> 2), t(ln & 3) {}
 
   // ---- units ---------------------------------------------------------------------------------------
-  __device__ void set_seq(int i) {
-    seq = i;
-    bool bad;
-    sp = span_of(a, i, &bad);
-    un = units_of<UT>(sp);
-  }
-  __device__ void seek(long long f) {
-    const int want = static_cast<int>(f / he_count);
-    int lo = 0, hi = a.rows;  // cum[lo] <= want < cum[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= want)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    set_seq(lo);
-    const long long rem = f - static_cast<long long>(cum[lo]) * he_count;
-    he = static_cast<int>(rem / un.total);
-    local = static_cast<int>(rem - static_cast<long long>(he) * un.total);
-  }
-  __device__ void advance() {
-    if (++local < un.total) return;
-    local = 0;
-    if (++he < he_count) return;
-    he = 0;
-    int i = seq + 1;
-    while (i < a.rows && cum[i + 1] == cum[i]) ++i;
-    if (i < a.rows) set_seq(i);
-  }
-  __device__ Unit fetch() const {
-    Unit u;
-    const int h = a.passes == 1 ? he : he / a.passes;
-    u.len = sp.len;
-    u.start = sp.start;
-    u.sink_end = sp.sink_end;
-    u.res = local >= un.q_units;
-    u.ok = true;
-    u.ks = u.vs = 0;
-    int n;
-    if (!u.res) {
-      int x = local;
-      if (x >= un.q_sink) x += un.q_gap;
-      u.tok0 = x * UT;
-      n = UT;
-      const int j = u.tok0 >> a.lg_r, in = u.tok0 & ((1 << a.lg_r) - 1);
-      long long blk;
-      if (a.block_table != nullptr) {
-        const int page = __ldg(a.block_table + static_cast<size_t>(seq) * a.max_blocks + j);  // j < max_blocks: span_of
-        u.ok = page >= 0 && page < a.num_pages;
-        blk = static_cast<long long>(u.ok ? page : 0) * a.heads + h;
-        if (!u.ok && lane == 0) report_status(a.status, KIVI_ERR_INTERNAL);
+  // Runs of plain successors are stepped through in registers; what changes at their ends is in shared memory.
+  __device__ __forceinline__ void fetch() {
+    if (!res) {
+      const uint32_t j = static_cast<uint32_t>(x) >> a.lg_upb;
+      if (table != nullptr) {
+        const int page = __ldg(table + j);  // j < max_blocks: span_of
+        ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
+        blk = static_cast<uint32_t>(ok ? page : 0) * static_cast<uint32_t>(a.heads) + hbase;
+        if (!ok && lane == 0) report_status(a.status, KIVI_ERR_INTERNAL);
       } else {
-        blk = (static_cast<long long>(seq) * a.heads + h) * a.blocks_per_head + j;
+        ok = true;
+        blk = hbase + j;
       }
-      u.off = ((blk << a.lg_r) + in) * (kHeadDim * BITS / 8);
-      u.ks = blk * (kHeadDim >> a.lg_gk) + ((32 * t) >> a.lg_gk);
-      u.vs = (blk << a.lg_r >> a.lg_gv) + ((in + PT * t) >> a.lg_gv);
+      off = static_cast<long long>(static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHalfBytes << a.lg_upb) +
+                                   (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * kHalfBytes);
     } else {
-      int x = local - un.q_units;
-      if (x >= un.r_sink) x += un.r_gap;
-      u.tok0 = sp.quant + x * kResTokens;
-      n = kResTokens;
-      u.ok = u.tok0 < sp.len;
-      u.off = (((static_cast<long long>(seq) * a.heads + h) << a.lg_r) + x * kResTokens) * (kHeadDim * 2);
-    }
-    u.full = u.tok0 + n <= u.sink_end || (u.tok0 >= u.start && u.tok0 + n <= u.len);
-    return u;
-  }
-  __device__ void issue_k(const Unit& u) {
-    if (!u.ok) return;
-    if (lane == 0) mbar_arrive_expect_tx(&S.bar[0], kHalfBytes);
-    __syncwarp();
-    if (!u.res) {
-      if (lane == 0) bulk_g2s(S.k, reinterpret_cast<const char*>(a.k_codes) + u.off, kHalfBytes, &S.bar[0]);
-    } else if (lane < kResTokens) {
-      bulk_g2s(S.k + lane * kKRow, reinterpret_cast<const char*>(a.k_res) + u.off + lane * 256, 256, &S.bar[0]);
+      off = static_cast<long long>(static_cast<unsigned long long>(blk) * static_cast<uint32_t>((kHeadDim * 2) << a.lg_r) +
+                                   static_cast<uint32_t>(x) * kHalfBytes);
     }
   }
-  __device__ void issue_v(const Unit& u) {
-    if (!u.ok) return;
-    if (lane == 0) mbar_arrive_expect_tx(&S.bar[1], kHalfBytes);
-    __syncwarp();
-    const char* src = u.res ? reinterpret_cast<const char*>(a.v_res) : reinterpret_cast<const char*>(a.v_codes);
-    if (lane < 4) bulk_g2s(S.v + lane * kVPieceStride, src + u.off + lane * kVPiece, kVPiece, &S.bar[1]);
+  __device__ __forceinline__ void take(const int4& r) {
+    x = r.x;
+    run_ = r.y;
+    res = r.w & 1;
+    ok = (r.w & 2) != 0;
+    if (res) {
+      blk = static_cast<uint32_t>(r.z);
+    } else {
+      hbase = static_cast<uint32_t>(r.z);
+      table = a.block_table == nullptr ? nullptr : a.block_table + static_cast<size_t>(S.cur.seq) * a.max_blocks;
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    ++steps_;
+    if (run_ > 0) {
+      --run_;
+      ++x;
+    } else {
+      take(next_run<UT>(a, S.cur, steps_));
+      steps_ = 0;
+    }
+  }
+
+  // Copies of a unit's halves, 16 bytes per lane and step; a group is committed whether or not there are any.
+  __device__ __forceinline__ void issue_k(bool any) {
+    if (any && ok) {
+      const uint32_t dst = smem_u32(S.k);
+      if (!res) {
+        const char* src = reinterpret_cast<const char*>(a.k_codes) + off + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy16(dst + 16 * lane + 512 * i, src + 512 * i);
+      } else {
+        const char* src = reinterpret_cast<const char*>(a.k_res) + off + 16 * lane;
+#pragma unroll 1  // a loop, so that the paths stay branches and not sixteen predicated copies
+        for (int i = 0; i < 8; ++i) copy16(dst + (lane >> 4) * kRow + (lane & 15) * 16 + 2 * kRow * i, src + 512 * i);
+      }
+    }
+    copies_commit();
+  }
+  __device__ __forceinline__ void issue_v(bool any) {
+    if (any && ok) {
+      const uint32_t dst = smem_u32(S.v);
+      if (!res) {
+        const char* src = reinterpret_cast<const char*>(a.v_codes) + off + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy16(dst + (i >> 1) * kVPieceStride + (i & 1) * 512 + 16 * lane, src + 512 * i);
+      } else {
+        const char* src = reinterpret_cast<const char*>(a.v_res) + off + 16 * lane;
+#pragma unroll 1  // a loop, so that the paths stay branches and not sixteen predicated copies
+        for (int i = 0; i < 8; ++i) copy16(dst + (lane >> 4) * kRow + (lane & 15) * 16 + 2 * kRow * i, src + 512 * i);
+      }
+    }
+    copies_commit();
   }
   // (s, z) of this lane's piece: K channels 32 t .. 32 t + 31 and V tokens PT t .. PT t + PT - 1
-  __device__ void load_pairs(const Unit& u, uint32_t& kp, uint32_t& vp) const {
-    kp = vp = 0;
-    if (!u.ok || u.res) return;
-    kp = static_cast<uint32_t>(__ldg(a.k_scale + u.ks)) | (static_cast<uint32_t>(__ldg(a.k_zero + u.ks)) << 16);
-    vp = static_cast<uint32_t>(__ldg(a.v_scale + u.vs)) | (static_cast<uint32_t>(__ldg(a.v_zero + u.vs)) << 16);
+  __device__ __forceinline__ void load_pairs(uint32_t& kp, uint32_t& vp) const {
+    if (!ok || res) return;
+    const uint32_t in = (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * UT;
+    const size_t ks = static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHeadDim >> a.lg_gk) + ((32 * t) >> a.lg_gk);
+    const size_t vs = static_cast<unsigned long long>(blk) * (1u << (a.lg_r - a.lg_gv)) + ((in + PT * t) >> a.lg_gv);
+    kp = static_cast<uint32_t>(__ldg(a.k_scale + ks)) | (static_cast<uint32_t>(__ldg(a.k_zero + ks)) << 16);
+    vp = static_cast<uint32_t>(__ldg(a.v_scale + vs)) | (static_cast<uint32_t>(__ldg(a.v_zero + vs)) << 16);
   }
-  __device__ static bool seen(const Unit& u, int tok) { return tok < u.len && (tok < u.sink_end || tok >= u.start); }
+  __device__ __forceinline__ bool seen(int tok) const {
+    const Span& n = S.cur.now;
+    return tok < n.len && (tok < n.sink_end || tok >= n.start);
+  }
 
   // ---- the head's queries ----------------------------------------------------------------------------
   __device__ void start_head() {
-    const int h = he / a.passes, pass = he - h * a.passes;
+    const int he = S.cur.he_now, h = he / a.passes, pass = he - h * a.passes;
     bool bad = false;
-    const int row = q_row(a, seq, &bad);
+    const int row = q_row(a, S.cur.seq_now, &bad);
     const int q0 = pass * a.per_pass, nq = min(a.per_pass, a.gqa - q0);
     const uint16_t* base = a.q + (static_cast<size_t>(row) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0) * kHeadDim;
     __syncwarp();  // the previous head's raw queries are no longer read
@@ -347,17 +418,21 @@ struct Attender {
       big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
       big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
       const int e = big > 0.f ? (__float_as_int(big) >> 23) - 127 : 0;  // -24 .. 16
+      uint32_t qh[16];
 #pragma unroll
       for (int x = 0; x < KW; ++x)
 #pragma unroll
         for (int j = 0; j < HP; ++j) {
           const float sc = pow2i(6 - e - pair_shift<BITS>(j));
-          qh[b][x * HP + j] = pack_h2(f[x * P + j] * sc, f[x * P + j + HP] * sc);
+          qh[x * HP + j] = pack_h2(f[x * P + j] * sc, f[x * P + j + HP] * sc);
         }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S.qh[b][i][lane] = make_uint4(qh[4 * i], qh[4 * i + 1], qh[4 * i + 2], qh[4 * i + 3]);
       qe[b] = __shfl_sync(kFull, e, 8 * t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) qs[b][i] = a.qscale * __shfl_sync(kFull, sum, 8 * t + i);
-      m[b] = kNoMax;
+      m[b] = 0.f;
+      thr[b] = -INFINITY;  // any logit sets the reference
       l[b] = Z[b] = 0.f;
 #pragma unroll
       for (int v8 = 0; v8 < 8; ++v8)
@@ -368,19 +443,26 @@ struct Attender {
     __syncwarp();
   }
 
-  // o, l and Z move to a new running maximum and V scale exponent.
-  __device__ __forceinline__ void raise(int b, float mu, float escale) {
+  // Where a logit (over m) passes the threshold, m moves up to the largest (the first time: to wherever that is), and
+  // o, l and Z with it.  Returns how far.
+  __device__ __forceinline__ float raise(int b, float mu) {
     float mx = fmaxf(mu, __shfl_xor_sync(kFull, mu, 4));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-    const float mn = fmaxf(m[b], mx), al = ex2(m[b] - mn), ao = al * escale;
-    m[b] = mn;
+    if (!(mx > thr[b])) return 0.f;
+    thr[b] = kSlack;
+    m[b] += mx;
+    const float al = ex2(-fmaxf(mx, 0.f));  // the first time o, l and Z are zero
     l[b] *= al;
     Z[b] *= al;
+    scale_o(b, al);
+    return mx;
+  }
+  __device__ __forceinline__ void scale_o(int b, float f) {
 #pragma unroll
     for (int v8 = 0; v8 < 8; ++v8)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[b][v8][i] *= ao;
+      for (int i = 0; i < 4; ++i) o[b][v8][i] *= f;
   }
 
   // Slot of P operand vector (column n, code pair jl of word rows of lane tt): conflict-free for the
@@ -392,16 +474,17 @@ struct Attender {
   // ---- K half of a quantized unit: logits, softmax, P operands ------------------------------------------
   // Tile i = (tb, x, jj) (2 bits) or (tb, x) holds on rows g and g + 8 the tokens of pair j = 4 jj + g % 4 (g % 4)
   // of word row 2 tt + x, tt = 2 (g / 4) + tb: what lane tt of the V product needs as one operand register.
-  __device__ void quant_k(const Unit& u, uint32_t kp, uint32_t vp) {
-    const int jl = g & 3, tt0 = (g >> 2) * 2;
-    if (!u.full) {  // V pieces that are hidden whole have no say (their s and z may be anything)
-      const int p0 = u.tok0 + PT * t;
-      if (p0 >= u.sink_end && p0 + PT <= u.start) vp = 0;
+  __device__ __forceinline__ void quant_k(int ux, uint32_t kp, uint32_t vp) {
+    const int jl = g & 3, tt0 = (g >> 2) * 2, tok0 = ux * UT;
+    const bool full = ux >= full_from || ux < sink_full;
+    if (!full) {  // V pieces that are hidden whole have no say (their s and z may be anything)
+      const int p0 = tok0 + PT * t;
+      if (p0 >= S.cur.now.sink_end && p0 + PT <= S.cur.now.start) vp = 0;
     }
     const unsigned ksm = __reduce_max_sync(kFull, kp & 0xFFFFu), vsm = __reduce_max_sync(kFull, vp & 0xFFFFu);
     const int ek = max(1, static_cast<int>(ksm >> 10)), ev = max(1, static_cast<int>(vsm >> 10));
     const __half2 sh = __float2half2_rn(h2f(static_cast<uint16_t>(kp)) * pow2i(22 - ek));
-    const __half2 shl = (g & 1) ? sh : __float2half2_rn(0.f);
+    const __half2 nsh = (g & 1) ? __hneg2(sh) : __float2half2_rn(0.f);
     float z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = h2f(static_cast<uint16_t>(__shfl_sync(kFull, kp, i) >> 16));
@@ -410,72 +493,102 @@ struct Attender {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const __half2 q2 = as_h2(qh[b][i]);
-        kb[b][i] = as_u32(__hfma2(q2, sh, __hneg2(__hmul2(q2, shl))));  // even columns: q s rounded; odd: the rest
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q4 = S.qh[b][i][lane];
+        const uint32_t w[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          kb[b][4 * i + j] = as_u32(__hfma2(as_h2(w[j]), sh, __hmul2(as_h2(w[j]), nsh)));  // even columns: q s rounded; odd: the rest
       }
       inv[b] = a.qscale * pow2i(qe[b] + ek - 4);
-      cst[b] = fmaf(z[3], qs[b][3], fmaf(z[2], qs[b][2], fmaf(z[1], qs[b][1], z[0] * qs[b][0])));
+      cst[b] = fmaf(z[3], qs[b][3], fmaf(z[2], qs[b][2], fmaf(z[1], qs[b][1], z[0] * qs[b][0]))) - m[b];
     }
     const uint8_t* kt = S.k + ((g >> 2) * (UT / 2) + jl) * (16 * BITS) + 4 * KW * t;
+    // two tiles at a time: two independent chains of sums per column block
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int off = BITS == 2 ? (i >> 2) * 1024 + ((i >> 1) & 1) * 512 + (i & 1) * 128 : (i >> 1) * 1024 + (i & 1) * 512;
-      uint32_t wg[KW], wh[KW];
-      if constexpr (BITS == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(kt + off), y = *reinterpret_cast<const uint2*>(kt + off + 256);
-        wg[0] = x.x, wg[1] = x.y, wh[0] = y.x, wh[1] = y.y;
-      } else {
-        const uint4 x = *reinterpret_cast<const uint4*>(kt + off), y = *reinterpret_cast<const uint4*>(kt + off + 256);
-        wg[0] = x.x, wg[1] = x.y, wg[2] = x.z, wg[3] = x.w, wh[0] = y.x, wh[1] = y.y, wh[2] = y.z, wh[3] = y.w;
+    for (int i0 = 0; i0 < MT; i0 += 2) {
+      uint32_t w[2][2][KW], up[2][2][KW];  // [tile][row g, g + 8][word]
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = i0 + i;
+        const int off = BITS == 2 ? (n >> 2) * 1024 + ((n >> 1) & 1) * 512 + (n & 1) * 128 : (n >> 1) * 1024 + (n & 1) * 512;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          if constexpr (BITS == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(kt + off + 256 * y);
+            w[i][y][0] = x.x, w[i][y][1] = x.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(kt + off + 256 * y);
+            w[i][y][0] = x.x, w[i][y][1] = x.y, w[i][y][2] = x.z, w[i][y][3] = x.w;
+          }
+        }
       }
-      float c[NB][4];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) c[b][0] = c[b][1] = c[b][2] = c[b][3] = 0.f;
+      float c[2][NB][4];
 #pragma unroll
       for (int x = 0; x < KW; ++x) {
-        uint32_t ag[HP], ah[HP];
-        code_pairs<BITS>(wg[x], ag);
-        code_pairs<BITS>(wh[x], ah);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) up[i][y][x] = upper_codes<BITS>(w[i][y][x]);
 #pragma unroll
         for (int j = 0; j < HP; j += 2)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) mma16(c[b], ag[j], ah[j], ag[j + 1], ah[j + 1], kb[b][x * HP + j], kb[b][x * HP + j + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = code_pair<BITS>(w[i][0][x], up[i][0][x], j), a1 = code_pair<BITS>(w[i][1][x], up[i][1][x], j);
+            const uint32_t a2 = code_pair<BITS>(w[i][0][x], up[i][0][x], j + 1), a3 = code_pair<BITS>(w[i][1][x], up[i][1][x], j + 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if (x == 0 && j == 0)
+                mma16_first(c[i][b], a0, a1, a2, a3, kb[b][0], kb[b][1]);
+              else
+                mma16(c[i][b], a0, a1, a2, a3, kb[b][x * HP + j], kb[b][x * HP + j + 1]);
+            }
+          }
       }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        lg[b][i][0] = fmaf(c[b][0] + c[b][1], inv[b], cst[b]);
-        lg[b][i][1] = fmaf(c[b][2] + c[b][3], inv[b], cst[b]);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          lg[b][i0 + i][0] = fmaf(c[i][b][0] + c[i][b][1], inv[b], cst[b]);
+          lg[b][i0 + i][1] = fmaf(c[i][b][2] + c[i][b][3], inv[b], cst[b]);
+        }
     }
-    if (!u.full) {
+    if (!full) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int tok = BITS == 2 ? u.tok0 + 32 * (tt0 + (i >> 2)) + 16 * ((i >> 1) & 1) + 4 * (i & 1) + jl
-                                  : u.tok0 + 16 * (tt0 + (i >> 1)) + 8 * (i & 1) + jl;
+        const int tok = BITS == 2 ? tok0 + 32 * (tt0 + (i >> 2)) + 16 * ((i >> 1) & 1) + 4 * (i & 1) + jl
+                                  : tok0 + 16 * (tt0 + (i >> 1)) + 8 * (i & 1) + jl;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (!seen(u, tok + HP * y))
+          if (!seen(tok + HP * y))
 #pragma unroll
             for (int b = 0; b < NB; ++b) lg[b][i][y] = -INFINITY;
       }
     }
     float mu[NB];
-    bool up = ev > eref;
+    bool above = ev > eref;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       mu[b] = lg[b][0][0];
 #pragma unroll
       for (int i = 0; i < MT; ++i) mu[b] = fmaxf(mu[b], fmaxf(lg[b][i][0], lg[b][i][1]));
-      up = up || mu[b] > m[b];
+      above = above || mu[b] > thr[b];
     }
-    if (__any_sync(kFull, up)) {
+    if (__any_sync(kFull, above)) {
       const float escale = pow2i(min(0, eref - ev));
       eref = max(eref, ev);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) raise(b, mu[b], escale);
+      for (int b = 0; b < NB; ++b) {
+        const float by = raise(b, mu[b]);
+        scale_o(b, escale);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          lg[b][i][0] -= by;
+          lg[b][i][1] -= by;
+        }
+      }
     }
-    const float kscale = pow2i(28 - eref);
+    const float kscale = pow2i(24 - eref);
     uint32_t vq[2] = {__shfl_sync(kFull, vp, tt0), __shfl_sync(kFull, vp, tt0 + 1)};
     constexpr int JJ = BITS == 2 ? 2 : 1;
     float fac[2][JJ];
@@ -498,7 +611,7 @@ struct Attender {
         float ps = 0.f;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) {
-          const float p0 = ex2(lg[b][tb * HALF + i][0] - m[b]), p1 = ex2(lg[b][tb * HALF + i][1] - m[b]);
+          const float p0 = ex2(lg[b][tb * HALF + i][0]), p1 = ex2(lg[b][tb * HALF + i][1]);
           ps += p0 + p1;
           const float f = fac[tb][JJ == 2 ? i & 1 : 0], x0 = p0 * f, x1 = p1 * f;
           hi[i] = pack_h2(x0, x1);
@@ -520,47 +633,72 @@ struct Attender {
   }
 
   // ---- V half of a quantized unit: tile v8 holds channels 16 g + 2 v8 (row g) and 16 g + 2 v8 + 1 (row g + 8) ----
-  __device__ void quant_v() {
-    uint32_t pb[NB][2][HP];
+  // A k chunk takes the two pairs that one 8-byte part of a P vector holds: pairs jl and jl + 4 of word row x (2 bits),
+  // pair jl of both word rows (4 bits).
+  __device__ __forceinline__ void quant_v() {
+    uint32_t pb[NB][4][BITS == 2 ? 4 : 2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int jl = 0; jl < 4; ++jl) {
         if constexpr (BITS == 2) {
           const uint4 x = S.p[b][p_slot(g, jl, t)];
-          pb[b][0][jl] = x.x, pb[b][0][4 + jl] = x.y, pb[b][1][jl] = x.z, pb[b][1][4 + jl] = x.w;
+          pb[b][jl][0] = x.x, pb[b][jl][1] = x.y, pb[b][jl][2] = x.z, pb[b][jl][3] = x.w;
         } else {
           const uint2 x = reinterpret_cast<const uint2*>(S.p[b])[p_slot(g, jl, t)];
-          pb[b][0][jl] = x.x, pb[b][1][jl] = x.y;
+          pb[b][jl][0] = x.x, pb[b][jl][1] = x.y;
         }
       }
     const uint8_t* vt = S.v + t * kVPieceStride + 64 * g;
+    if constexpr (BITS == 2) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          uint32_t up[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up[e] = upper_codes<BITS>(w[e]);
+#pragma unroll
+          for (int jl = 0; jl < 4; ++jl)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const uint32_t a0 = code_pair<BITS>(w[e], up[e], jl), a1 = code_pair<BITS>(w[e + 1], up[e + 1], jl);
+              const uint32_t a2 = code_pair<BITS>(w[e], up[e], jl + 4), a3 = code_pair<BITS>(w[e + 1], up[e + 1], jl + 4);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16(o[b][2 * i + e / 2], a0, a1, a2, a3, pb[b][jl][2 * x], pb[b][jl][2 * x + 1]);
+            }
+        }
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        uint32_t w[2][4], up[2][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t ag[HP], ah[HP];
-          code_pairs<BITS>(w[2 * e], ag);
-          code_pairs<BITS>(w[2 * e + 1], ah);
+        for (int x = 0; x < 2; ++x) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
+          w[x][0] = w4.x, w[x][1] = w4.y, w[x][2] = w4.z, w[x][3] = w4.w;
 #pragma unroll
-          for (int j = 0; j < HP; j += 2)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              mma16(o[b][2 * i + e], ag[j], ah[j], ag[j + 1], ah[j + 1], pb[b][x][j], pb[b][x][j + 1]);
+          for (int e = 0; e < 4; ++e) up[x][e] = upper_codes<BITS>(w[x][e]);
         }
+#pragma unroll
+        for (int jl = 0; jl < 4; ++jl)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const uint32_t a0 = code_pair<BITS>(w[0][e], up[0][e], jl), a1 = code_pair<BITS>(w[0][e + 1], up[0][e + 1], jl);
+            const uint32_t a2 = code_pair<BITS>(w[1][e], up[1][e], jl), a3 = code_pair<BITS>(w[1][e + 1], up[1][e + 1], jl);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16(o[b][2 * i + e / 2], a0, a1, a2, a3, pb[b][jl][0], pb[b][jl][1]);
+          }
       }
+    }
   }
 
-  // ---- residual units: K on the tensor cores with the raw queries, V with fp32 multiply-adds ------------
-  __device__ void res_k(const Unit& u, float (&p)[NB][2]) {
+  // ---- residual units, on the tensor cores too: K rows with the raw queries, V rows transposed on the way ----------
+  // Logits of rows g and g + 8 for query t, as weights times 2^10 in p.
+  __device__ __forceinline__ void res_k(int ux, float (&p)[NB][2], float (&r)[NB][8][4]) {
     float c[NB][4];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) c[b][0] = c[b][1] = c[b][2] = c[b][3] = 0.f;
-    const uint32_t row = smem_u32(S.k) + (lane & 15) * kKRow + (lane >> 4) * 16;
+    const uint32_t row = smem_u32(S.k) + (lane & 15) * kRow + (lane >> 4) * 16;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t x[4];
@@ -569,58 +707,112 @@ struct Attender {
       for (int b = 0; b < NB; ++b) {
         const uint32_t* q = reinterpret_cast<const uint32_t*>(S.q[b] + (g >> 1) * kQRow) + 8 * i + t;
         const uint32_t b0 = (g & 1) ? 0u : q[0], b1 = (g & 1) ? 0u : q[4];
-        mma16(c[b], x[0], x[1], x[2], x[3], b0, b1);
+        if (i == 0)
+          mma16_first(c[b], x[0], x[1], x[2], x[3], b0, b1);
+        else
+          mma16(c[b], x[0], x[1], x[2], x[3], b0, b1);
       }
     }
-    const bool s0 = seen(u, u.tok0 + g), s1 = seen(u, u.tok0 + g + 8);
-    bool up = false;
-    float mu[NB], lg[NB][2];
+    const int tok0 = S.cur.now.quant + ux * kResTokens;
+    const bool s0 = seen(tok0 + g), s1 = seen(tok0 + g + 8);
+    bool above = false;
+    float mu[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      lg[b][0] = s0 ? (c[b][0] + c[b][1]) * a.qscale : -INFINITY;
-      lg[b][1] = s1 ? (c[b][2] + c[b][3]) * a.qscale : -INFINITY;
-      mu[b] = fmaxf(lg[b][0], lg[b][1]);
-      up = up || mu[b] > m[b];
+      p[b][0] = s0 ? fmaf(c[b][0], a.qscale, -m[b]) : -INFINITY;
+      p[b][1] = s1 ? fmaf(c[b][2], a.qscale, -m[b]) : -INFINITY;
+      mu[b] = fmaxf(p[b][0], p[b][1]);
+      above = above || mu[b] > thr[b];
     }
-    if (__any_sync(kFull, up)) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) raise(b, mu[b], 1.f);
-    }
-    const float oscale = pow2i(4 - eref);  // o carries 2^(28 - eref - 24)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float p0 = ex2(lg[b][0] - m[b]), p1 = ex2(lg[b][1] - m[b]);
-      l[b] += p0 + p1;
-      p[b][0] = p0 * oscale;
-      p[b][1] = p1 * oscale;
-    }
-  }
-  __device__ void res_v(const Unit& u, const float (&p)[NB][2]) {
-#pragma unroll 1
-    for (int j = 0; j < kResTokens; ++j) {
-      if (!seen(u, u.tok0 + j)) continue;  // the same for every lane; rows that are hidden may hold anything
-      const uint4* src = reinterpret_cast<const uint4*>(S.v + (j >> 2) * kVPieceStride + (j & 3) * 256 + 32 * g);
-      const uint4 x = src[0], y = src[1];
-      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    if (__any_sync(kFull, above)) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float pj = __shfl_sync(kFull, j < 8 ? p[b][0] : p[b][1], (j & 7) * 4 + t);
+        const float by = raise(b, mu[b]), al = ex2(-fmaxf(by, 0.f));
+        p[b][0] -= by;
+        p[b][1] -= by;
 #pragma unroll
-        for (int v8 = 0; v8 < 8; ++v8) {
-          const float2 f = unpack_h2(w[v8]);
-          o[b][v8][0] = fmaf(pj, f.x, o[b][v8][0]);
-          o[b][v8][2] = fmaf(pj, f.y, o[b][v8][2]);
-        }
+        for (int v8 = 0; v8 < 8; ++v8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[b][v8][i] *= al;
       }
     }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      p[b][0] = ex2(p[b][0]);
+      p[b][1] = ex2(p[b][1]);
+      l[b] += p[b][0] + p[b][1];
+      p[b][0] *= 1024.f;
+      p[b][1] *= 1024.f;
+    }
+  }
+  // r: tile v8 holds channels 16 v8 + g (row g) and 16 v8 + 8 + g (row g + 8), columns as o; times 2^10.
+  __device__ __forceinline__ void res_v(int ux, const float (&p)[NB][2], float (&r)[NB][8][4]) {
+    const int tok0 = S.cur.now.quant + ux * kResTokens;
+    if (tok0 < S.cur.now.start || tok0 + kResTokens > S.cur.now.len) {  // hidden rows may hold anything: clear them
+#pragma unroll 1
+      for (int j = 0; j < kResTokens; ++j)
+        if (!seen(tok0 + j)) *reinterpret_cast<uint2*>(S.v + j * kRow + 8 * lane) = make_uint2(0, 0);
+      __syncwarp();
+    }
+    uint32_t pb[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __shfl_sync(kFull, p[b][i >> 1], 4 * (2 * t + (i & 1)) + (g >> 1));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t hi = pack_h2(x[2 * i], x[2 * i + 1]);
+        const float2 f = unpack_h2(hi);
+        pb[b][i] = (g & 1) ? pack_h2(x[2 * i] - f.x, x[2 * i + 1] - f.y) : hi;
+      }
+    }
+    const uint32_t row = smem_u32(S.v) + ((lane & 7) + (lane >> 4) * 8) * kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int v8 = 0; v8 < 8; ++v8) {
+      uint32_t x[4];
+      ldmatrix4_trans(x, row + 32 * v8);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) mma16(r[b][v8], x[0], x[1], x[2], x[3], pb[b][0], pb[b][1]);
+    }
+  }
+  // The residual rows' share of the output, through shared memory to the layout of o.
+  __device__ __forceinline__ void add_residual(const float (&r)[NB][8][4]) {
+    float* buf = reinterpret_cast<float*>(S.p[0]);  // 4 queries at a time of 64 channels: 1 KB
+    const float f = pow2i(-10 - eref);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          buf[64 * t + 16 * v + g] = (r[b][4 * half + v][0] + r[b][4 * half + v][1]) * f;
+          buf[64 * t + 16 * v + 8 + g] = (r[b][4 * half + v][2] + r[b][4 * half + v][3]) * f;
+        }
+        __syncwarp();
+        if ((g >> 2) == half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(buf + 64 * t + 16 * (g & 3) + 4 * i);
+            o[b][2 * i][0] += x.x;
+            o[b][2 * i][2] += x.y;
+            o[b][2 * i + 1][0] += x.z;
+            o[b][2 * i + 1][2] += x.w;
+          }
+        }
+      }
+    __syncwarp();
   }
 
   // ---- the end of a head's segment -----------------------------------------------------------------------
   // Lane (g, t): o of query t (each column block), channels 16 g .. 16 g + 15.
   __device__ void finish(bool whole, int slot) {
-    const int h = he_now / a.passes, pass = he_now - h * a.passes;
+    const int he = S.cur.he_now, h = he / a.passes, pass = he - h * a.passes;
     const int q0 = pass * a.per_pass, nq = min(a.per_pass, a.gqa - q0);
-    const float back = pow2i(eref - 4);
+    bool bad = false;
+    const int row = q_row(a, S.cur.seq_now, &bad);
+    const float back = pow2i(eref);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float ls = l[b], zs = Z[b];
@@ -643,12 +835,12 @@ struct Attender {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = pack_h2((f[2 * i] + zs) * inv, (f[2 * i + 1] + zs) * inv);
         uint4* dst = reinterpret_cast<uint4*>(
-            a.out + (static_cast<size_t>(row_now) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0 + qi) * kHeadDim + 16 * g);
+            a.out + (static_cast<size_t>(row) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0 + qi) * kHeadDim + 16 * g);
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
         float* dst = a.partials + ((worker * 2 + slot) * NQ + qi) * kPart;
-        if (g == 0) *reinterpret_cast<float4*>(dst) = make_float4(m[b], ls, zs, 0.f);
+        if (g == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m[b], ls, zs, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(dst + 4 + 16 * g + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
@@ -711,98 +903,103 @@ struct Attender {
                                 4 * lane) =
           make_uint2(pack_h2((acc[0] + zs) * inv, (acc[1] + zs) * inv), pack_h2((acc[2] + zs) * inv, (acc[3] + zs) * inv));
     }
-    if (lane == 0) a.tickets[static_cast<size_t>(s) * he_count + e] = 0;
+    if (lane == 0) a.tickets[static_cast<size_t>(s) * a.heads * a.passes + e] = 0;
   }
 
-  __device__ bool wait(int which, uint32_t& phase) {
-    const bool ok = __all_sync(kFull, mbar_wait_bounded(&S.bar[which], phase, kWaitNs));
-    phase ^= 1;
-    return ok;
-  }
-
-  int he_now, row_now;
-
-  __device__ void run(long long w, long long nw, long long all) {
+  __device__ void run(long long w, long long nw, long long all, int seq0, long long rem) {
     worker = w;
     workers = nw;
     total = all;
-    const long long f0 = total * w / workers, f1 = total * (w + 1) / workers;
-    if (lane == 0) {
-      mbar_init(&S.bar[0], 1);
-      mbar_init(&S.bar[1], 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    const long long f0 = total * w / workers;
+    int left = static_cast<int>(total * (w + 1) / workers - f0);  // below 2^31: rows * units a head are
+    {
+      bool bad;
+      const int n = units_of<UT>(span_of(a, seq0, &bad)).total, he = static_cast<int>(rem / n);
+      take(enter<UT>(a, S.cur, seq0, he, static_cast<int>(rem - static_cast<long long>(he) * n), true));
+      steps_ = 0;
     }
-    __syncwarp();
-    seek(f0);
-    Unit nx = fetch();
-    issue_k(nx);
-    issue_v(nx);
-    uint32_t kp, vp;
-    load_pairs(nx, kp, vp);
+    fetch();
+    issue_k(true);
+    issue_v(true);
+    uint32_t kp = 0, vp = 0;
+    load_pairs(kp, vp);
     struct Head {
       int seq, he, units;
       long long f0;
     } pend[2];
     int npend = 0;
-    long long left = f1 - f0;
-    bool first = true;
+    long long at = f0;
     while (left > 0) {
-      const int s = seq, e = he, l0 = local, units = un.total;
-      const int count = static_cast<int>(min(left, static_cast<long long>(units - local)));
-      bool bad = false;
-      he_now = he;
-      row_now = q_row(a, seq, &bad);
+      Cursor& c = S.cur;
+      const int s = c.seq, e = c.he, l0 = c.local, units = c.un.total;
+      const int count = min(left, units - l0), nq = min(count, max(0, c.un.q_units - l0));
+      __syncwarp();
+      if (lane == 0) {
+        c.now = c.sp;
+        c.he_now = e;
+        c.seq_now = s;
+      }
+      __syncwarp();
+      full_from = (c.now.start + UT - 1) / UT;
+      sink_full = c.now.sink_end / UT;
       start_head();
-      for (int i = 0; i < count; ++i) {
-        const Unit cu = nx;
+      // K of the unit in hand, then V; the next unit's K is copied behind the one, its V behind the other
+#pragma unroll 1
+      for (int i = 0; i < nq; ++i) {
+        const int ux = x;
+        const bool good = ok, more = --left > 0;
         const uint32_t ckp = kp, cvp = vp;
-        const bool more = left - i > 1;
         if (more) {
           advance();
-          nx = fetch();
+          fetch();
         }
-        float p[NB][2];
-        if (cu.ok) {
-          if (!wait(0, kphase)) {
-            if (lane == 0) report_status(a.status, KIVI_ERR_DEVICE_TIMEOUT);
-            (void)mbar_wait_bounded(&S.bar[1], vphase, kWaitNs);  // no copy in flight when the warp ends
-            return;
-          }
-          if (!cu.res)
-            quant_k(cu, ckp, cvp);
-          else
-            res_k(cu, p);
-        }
+        copies_wait<1>();
+        if (good) quant_k(ux, ckp, cvp);
         __syncwarp();  // the K half has been read, and the P operands are written
-        if (more) {
-          issue_k(nx);
-          load_pairs(nx, kp, vp);
-        }
-        if (cu.ok) {
-          if (!wait(1, vphase)) {
-            if (lane == 0) report_status(a.status, KIVI_ERR_DEVICE_TIMEOUT);
-            if (more && nx.ok) (void)mbar_wait_bounded(&S.bar[0], kphase, kWaitNs);
-            return;
-          }
-          if (!cu.res)
-            quant_v();
-          else
-            res_v(cu, p);
-        }
+        issue_k(more);
+        if (more) load_pairs(kp, vp);
+        copies_wait<1>();
+        if (good) quant_v();
         __syncwarp();
-        if (more) issue_v(nx);
+        issue_v(more);
+      }
+      if (count > nq) {
+        float r[NB][8][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int v8 = 0; v8 < 8; ++v8) r[b][v8][0] = r[b][v8][1] = r[b][v8][2] = r[b][v8][3] = 0.f;
+#pragma unroll 1
+        for (int i = nq; i < count; ++i) {
+          const int ux = x;
+          const bool good = ok, more = --left > 0;
+          if (more) {
+            advance();
+            fetch();
+          }
+          float p[NB][2];
+          copies_wait<1>();
+          if (good) res_k(ux, p, r);
+          __syncwarp();
+          issue_k(more);
+          if (more) load_pairs(kp, vp);
+          copies_wait<1>();
+          if (good) res_v(ux, p, r);
+          __syncwarp();
+          issue_v(more);
+        }
+        add_residual(r);
       }
       const bool whole = count == units;
-      finish(whole, first ? 0 : 1);
+      finish(whole, at == f0 ? 0 : 1);
       if (!whole) {
         pend[npend].seq = s;
         pend[npend].he = e;
         pend[npend].units = units;
-        pend[npend].f0 = f1 - left - l0;
+        pend[npend].f0 = at - l0;
         ++npend;
       }
-      left -= count;
-      first = false;
+      at += count;
     }
     if (npend == 0) return;
     // one fence publishes this warp's partials before its tickets; the last part of a head joins it
@@ -812,7 +1009,7 @@ struct Attender {
     if (lane == 0) {
       for (int i = 0; i < npend; ++i) {
         const int others = static_cast<int>(worker_of(pend[i].f0 + pend[i].units - 1) - worker_of(pend[i].f0));
-        if (atomicAdd(a.tickets + static_cast<size_t>(pend[i].seq) * he_count + pend[i].he, 1) == others) last |= 1 << i;
+        if (atomicAdd(a.tickets + static_cast<size_t>(pend[i].seq) * a.heads * a.passes + pend[i].he, 1) == others) last |= 1 << i;
       }
       if (last) __threadfence();
     }
@@ -827,22 +1024,18 @@ struct Attender {
 
 template <int BITS, int NB>
 __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int W = attend_warps<NB>(), T = W * 32;
+  constexpr int W = attend_warps<NB>(), T = W * 32, UT = Attender<BITS, NB>::UT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = WarpSmem<BITS, NB>;
-  int* cum = reinterpret_cast<int*>(smem_raw + W * sizeof(Smem));
-  __shared__ int warp_sum[W];
+  __shared__ int warp_sum[W], cum[T + 1];  // units per head before each thread's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // units per head of every row, and their prefix sums (rows below 8193, sums below 2^31)
   const int per = (a.rows + T - 1) / T, r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
   int mine = 0;
   for (int i = r0; i < r1; ++i) {
-    bool bad = false, bad_row = false;
-    const int row = q_row(a, i, &bad_row);
-    const int n = row < 0 ? 0 : units_of<Attender<BITS, NB>::UT>(span_of(a, i, &bad)).total;
-    if ((bad || bad_row) && blockIdx.x == 0) report_status(a.status, KIVI_ERR_INTERNAL);
-    cum[i] = n;
-    mine += n;
+    bool bad = false;
+    if (q_row(a, i, &bad) >= 0) (void)span_of(a, i, &bad);
+    if (bad && blockIdx.x == 0) report_status(a.status, KIVI_ERR_INTERNAL);
+    mine += row_units<UT>(a, i);
   }
   int x = mine;
 #pragma unroll
@@ -854,28 +1047,38 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   __syncthreads();
   int before = x - mine;
   for (int i = 0; i < warp; ++i) before += warp_sum[i];
-  for (int i = r0; i < r1; ++i) {
-    const int n = cum[i];
-    cum[i] = before;
-    before += n;
-  }
-  if (r0 < a.rows && r1 == a.rows) cum[a.rows] = before;
+  cum[tid] = before;
+  if (tid == T - 1) cum[T] = before + mine;
   __syncthreads();
-  const long long total = static_cast<long long>(cum[a.rows]) * a.heads * a.passes;
+  const long long he_count = static_cast<long long>(a.heads) * a.passes;
+  const long long total = cum[T] * he_count;
   const long long workers = min(total, static_cast<long long>(gridDim.x) * W);
   // neighbouring workers on different SMs: few units spread over the GPU
   const long long worker = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
   if (worker >= workers) return;
-  Attender<BITS, NB> d(a, reinterpret_cast<Smem*>(smem_raw)[warp], cum, lane);
-  d.run(worker, workers, total);
+  // the row of the worker's first unit: its thread's rows by bisection, then one by one
+  const long long f0 = total * worker / workers;
+  const int want = static_cast<int>(f0 / he_count);
+  int lo = 0, hi = T;  // cum[lo] <= want < cum[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= want)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  int row = lo * per, first = cum[lo];
+  for (int n; first + (n = row_units<UT>(a, row)) <= want; ++row) first += n;
+  Attender<BITS, NB> d(a, reinterpret_cast<Smem*>(smem_raw)[warp], lane);
+  d.run(worker, workers, total, row, f0 - first * he_count);
 }
 
 template <int BITS, int NB>
 cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
-  const size_t smem = attend_warps<NB>() * sizeof(WarpSmem<BITS, NB>) + (static_cast<size_t>(a.rows) + 1) * sizeof(int);
-  static_assert(attend_warps<NB>() * sizeof(WarpSmem<BITS, NB>) + 8193 * 4 + 128 <= 232448, "a CTA holds 227 KB of shared memory");
+  constexpr int smem = attend_warps<NB>() * static_cast<int>(sizeof(WarpSmem<BITS, NB>));
+  static_assert(smem + 4 * (attend_warps<NB>() * 33 + 1) <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
   const cudaError_t e =
-      cudaFuncSetAttribute(attend_kernel<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      cudaFuncSetAttribute(attend_kernel<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   attend_kernel<BITS, NB><<<ctas, attend_warps<NB>() * 32, smem, stream>>>(a);
   return cudaGetLastError();
@@ -912,6 +1115,7 @@ cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* wor
   const Shape s = shape_of(a.max_rows, a.heads, a.gqa, max_units);
   a.passes = s.passes;
   a.per_pass = s.per_pass;
+  a.lg_upb = a.lg_r - (bits == 2 ? 7 : 6);
   a.tickets = static_cast<int32_t*>(workspace);
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(a.max_rows, a.heads, s));
   int dev = 0, sms = 0;

@@ -75,6 +75,7 @@ struct AttendArgs {
   int q_rows;
   int num_pages, max_blocks, blocks_per_head;
   int lg_r, lg_gk, lg_gv;
+  int lg_upb;  // log2 of the units per block (set by launch_attend)
   int window, sinks;  // window: INT32_MAX when every token is visible
   float qscale;       // softmax scale * log2(e)
 };
