@@ -45,15 +45,28 @@ constexpr float kSlack = 4.f;                     // logits may pass the referen
 #ifndef KIVI_ATTEND_WARPS
 #define KIVI_ATTEND_WARPS 12
 #endif
+#ifndef KIVI_ATTEND_WARPS_ONE
+#define KIVI_ATTEND_WARPS_ONE 16
+#endif
 template <int NB>
 __host__ __device__ constexpr int attend_warps() {
-  return NB == 1 ? KIVI_ATTEND_WARPS : 8;
+  return NB == 0 ? KIVI_ATTEND_WARPS_ONE : (NB == 1 ? KIVI_ATTEND_WARPS : 8);
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  return v;
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
@@ -83,6 +96,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const char* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -185,13 +201,12 @@ __device__ __forceinline__ int row_units(const AttendArgs& a, int i) {
   return q_row(a, i, &bad) < 0 ? 0 : units_of<UT>(span_of(a, i, &bad)).total;
 }
 
-// Where a warp is: the unit it fetched last (seq, head and pass he, index local of the head's units), and the span of
-// the head it works on, one unit behind.
+// Where a warp is: unit `local` of a head (KV head and query pass he) of row seq.
 struct Cursor {
   int seq, he, local;
+  int row, q0, queries;  // row of q and out, first query head and queries of the pass
   Units un;
-  Span sp, now;
-  int he_now, seq_now;
+  Span sp;
 };
 
 // The cursor at unit `local` of a head, for the whole warp: {index, plain successors, block or its base, 1: residual + 2: ok}.
@@ -199,24 +214,30 @@ template <int UT>
 __device__ __noinline__ int4 enter(const AttendArgs& a, Cursor& c, int seq, int he, int local, bool new_seq) {
   Units un;
   Span sp;
+  int row;
   if (new_seq) {
     bool bad;
     sp = span_of(a, seq, &bad);
     un = units_of<UT>(sp);
+    row = q_row(a, seq, &bad);
   } else {
     sp = c.sp;
     un = c.un;
+    row = c.row;
   }
+  const int h = a.passes == 1 ? he : he / a.passes, q0 = (he - h * a.passes) * a.per_pass;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     c.seq = seq;
     c.he = he;
     c.local = local;
+    c.row = row;
+    c.q0 = h * a.gqa + q0;
+    c.queries = min(a.per_pass, a.gqa - q0);
     c.sp = sp;
     c.un = un;
   }
   __syncwarp();
-  const int h = he / a.passes;
   const bool res = local >= un.q_units;
   const int r = res ? local - un.q_units : local, sink = res ? un.r_sink : un.q_sink, gap = res ? un.r_gap : un.q_gap;
   const int end = res ? un.total - un.q_units : un.q_units, x = r + (r >= sink ? gap : 0);
@@ -244,27 +265,29 @@ __device__ __noinline__ int4 next_run(const AttendArgs& a, Cursor& c, int steps)
   return enter<UT>(a, c, seq, he, local, new_seq);
 }
 
+// A warp's shared memory.  NB: column blocks of four queries; 0: one query on byte digits.
 template <int BITS, int NB>
 struct __align__(128) WarpSmem {
+  static constexpr int kQueries = NB == 0 ? 1 : 4 * NB;
   uint8_t k[kResTokens * kRow];
   uint8_t v[kResTokens * kRow];
-  uint4 p[NB][BITS == 2 ? 128 : 64];  // P operands: column, code pair and word rows (p_slot)
-  uint4 qh[NB][4][32];                // each lane's share of the K product's B operand, before s
-  uint8_t q[NB][4 * kQRow];           // the head's raw queries
-  Cursor cur;
+  uint8_t q[2][kQueries * kQRow];     // raw queries: of the head in hand, and of the next one as it arrives
+  uint4 p[NB == 0 ? 1 : NB][NB == 0 ? 32 : (BITS == 2 ? 128 : 64)];  // P operands
+  uint4 qh[NB == 0 ? 1 : NB][NB == 0 ? 1 : 4][32];                   // Q operands (NB > 0: before s, each lane's share)
+  uint4 zero4;                        // NB == 0: the operand of the other tile of a pair
+  Cursor cur, now;                    // of the unit fetched last, and of the head in hand
 };
 static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes, "a buffer holds either kind of half");
 
-template <int BITS, int NB>
-struct Attender {
-  static constexpr int P = 32 / BITS;               // codes per word
-  static constexpr int HP = P / 2;                  // code pairs per word
+// A warp's walk over its range of units: what is fetched when, where the halves land, and the ends of heads.  Core is the
+// arithmetic: start_head, quant_k, quant_v, Res (state of residual rows) with res_start, res_k, res_v and res_end, finish.
+template <int BITS, int NB, class Core>
+struct Walker {
+  static constexpr int P = 32 / BITS;                  // codes per word
   static constexpr int UT = attend_unit_tokens(BITS);  // tokens per quantized unit
-  static constexpr int PT = UT / 4;                 // tokens of two V word rows
-  static constexpr int MT = UT / 16;                // K tiles per unit
-  static constexpr int KW = kHeadDim / P / 4;       // K words per lane and token
-  static constexpr int NQ = 4 * NB;                 // queries a warp holds
+  static constexpr int PT = UT / 4;                    // tokens of two V word rows
   using Smem = WarpSmem<BITS, NB>;
+  static constexpr int NQ = Smem::kQueries;            // queries a warp holds
 
   const AttendArgs& a;
   Smem& S;
@@ -274,20 +297,15 @@ struct Attender {
   // the unit fetched last: its index among the row's units of codes or residual rows, how many plain successors it has,
   // whether it can be read, and where it is
   int x, run_, steps_;  // steps_: since the cursor was written
-  bool res, ok;
+  bool res, ok, head;     // head: its K half brings the head's queries
+  int slot;               // of S.q that the head fetched last has
   uint32_t blk, hbase;    // block; KV head (pages) or first block of the head (contiguous)
   long long off;          // bytes from the start of the K and V arrays
   const int32_t* table;   // the row's block table, or null
+  int slot_now;           // of S.q that the head in hand has
   int full_from, sink_full;  // units from the one and below the other are visible whole
 
-  // state of the head in hand: lane (g, t) is query t (of each column block) and channels 16 g .. 16 g + 15.
-  // Weights are 2^(logit - m): m is the largest logit when it was last raised, by at most kSlack below the largest.
-  float m[NB], thr[NB], l[NB], Z[NB], o[NB][8][4];
-  float qs[NB][4];   // scale * log2 e * sum of q over channels 32 i .. 32 i + 31
-  int qe[NB];        // exponent of the largest |q|
-  int eref;          // exponent field of the largest V scale so far: o carries 2^-eref (P operands 2^(24 - eref))
-
-  __device__ Attender(const AttendArgs& args, Smem& smem, int ln) : a(args), S(smem), lane(ln), g(ln >> 2), t(ln & 3) {}
+  __device__ Walker(const AttendArgs& args, Smem& smem, int ln) : a(args), S(smem), lane(ln), g(ln >> 2), t(ln & 3) {}
 
   // ---- units ---------------------------------------------------------------------------------------
   // Runs of plain successors are stepped through in registers; what changes at their ends is in shared memory.
@@ -315,6 +333,7 @@ struct Attender {
     run_ = r.y;
     res = r.w & 1;
     ok = (r.w & 2) != 0;
+    head = S.cur.local == 0;
     if (res) {
       blk = static_cast<uint32_t>(r.z);
     } else {
@@ -327,6 +346,7 @@ struct Attender {
     if (run_ > 0) {
       --run_;
       ++x;
+      head = false;
     } else {
       take(next_run<UT>(a, S.cur, steps_));
       steps_ = 0;
@@ -335,6 +355,18 @@ struct Attender {
 
   // Copies of a unit's halves, 16 bytes per lane and step; a group is committed whether or not there are any.
   __device__ __forceinline__ void issue_k(bool any) {
+    if (any && head) {  // NQ rows of 16 chunks (fewer queries: rows of zeros)
+      slot ^= 1;
+      const Cursor& c = S.cur;
+      const char* src = reinterpret_cast<const char*>(a.q) + (static_cast<size_t>(c.row) * a.heads * a.gqa + c.q0) * (kHeadDim * 2);
+#pragma unroll
+      for (int i = 0; i < (NQ + 1) / 2; ++i) {
+        const int qi = 2 * i + (lane >> 4);
+        if (qi >= NQ) break;
+        copy16_or_zeros(smem_u32(S.q[slot]) + qi * kQRow + (lane & 15) * 16, src + (qi < c.queries ? qi * 256 + (lane & 15) * 16 : 0),
+                        qi < c.queries);
+      }
+    }
     if (any && ok) {
       const uint32_t dst = smem_u32(S.k);
       if (!res) {
@@ -358,8 +390,11 @@ struct Attender {
         for (int i = 0; i < 8; ++i) copy16(dst + (i >> 1) * kVPieceStride + (i & 1) * 512 + 16 * lane, src + 512 * i);
       } else {
         const char* src = reinterpret_cast<const char*>(a.v_res) + off + 16 * lane;
-#pragma unroll 1  // a loop, so that the paths stay branches and not sixteen predicated copies
-        for (int i = 0; i < 8; ++i) copy16(dst + (lane >> 4) * kRow + (lane & 15) * 16 + 2 * kRow * i, src + 512 * i);
+        const Span& n = S.cur.sp;
+        const int tok = n.quant + x * kResTokens + (lane >> 4);
+#pragma unroll 1  // hidden rows may hold anything: zeros instead
+        for (int i = 0; i < 8; ++i)
+          copy16_or_zeros(dst + (lane >> 4) * kRow + (lane & 15) * 16 + 2 * kRow * i, src + 512 * i, seen(n, tok + 2 * i));
       }
     }
     copies_commit();
@@ -373,32 +408,232 @@ struct Attender {
     kp = static_cast<uint32_t>(__ldg(a.k_scale + ks)) | (static_cast<uint32_t>(__ldg(a.k_zero + ks)) << 16);
     vp = static_cast<uint32_t>(__ldg(a.v_scale + vs)) | (static_cast<uint32_t>(__ldg(a.v_zero + vs)) << 16);
   }
-  __device__ __forceinline__ bool seen(int tok) const {
-    const Span& n = S.cur.now;
+  __device__ static __forceinline__ bool seen(const Span& n, int tok) {
     return tok < n.len && (tok < n.sink_end || tok >= n.start);
   }
 
+  // Worker whose range holds unit f: ranges start at floor(total w / workers).
+  __device__ static __forceinline__ long long worker_of(long long f, long long workers, long long total) {
+    return ((f + 1) * workers + total - 1) / total - 1;
+  }
+
+  // The workers that hold a part of a head left one partial each: the first of them in its slot 1
+  // unless its range starts with the head, the others in their slot 0.  Lane i reads (m, l, Z) of part i;
+  // the o rows follow with 16 loads in flight.
+  __device__ __noinline__ static void merge(const AttendArgs& a, int s, int e, int units, long long f0, long long workers,
+                                            long long total) {
+    const int lane = threadIdx.x & 31;
+    const long long w0 = worker_of(f0, workers, total), w1 = worker_of(f0 + units - 1, workers, total);
+    const int parts = static_cast<int>(w1 - w0 + 1);
+    const long long first = w0 * 2 + (total * w0 / workers >= f0 ? 0 : 1);
+    const int h = e / a.passes, p0 = (e - h * a.passes) * a.per_pass, nq = min(a.per_pass, a.gqa - p0);
+    bool bad = false;
+    uint16_t* out = a.out + (static_cast<size_t>(q_row(a, s, &bad)) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + p0) * kHeadDim;
+    auto part = [&](int k, int q) { return a.partials + ((k == 0 ? first : (w0 + k) * 2) * NQ + q) * kPart; };
+    constexpr int CH = 16 / NQ;  // parts whose rows are in flight together
+    float mx[NQ], ls[NQ], zs[NQ], acc[NQ][4];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      mx[q] = kNoMax;
+      ls[q] = zs[q] = acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    }
+    if (parts > 32) {  // the largest reference first; up to 32 parts find it below
+      for (int k = lane; k < parts; k += 32)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (q < nq) mx[q] = fmaxf(mx[q], __ldcg(part(k, q)));
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) mx[q] = warp_max(mx[q]);
+    }
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      float4 x[NQ];
+      float w[NQ];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        x[q] = q < nq && k0 + lane < parts ? __ldcg(reinterpret_cast<const float4*>(part(k0 + lane, q))) : make_float4(kNoMax, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (parts <= 32) mx[q] = warp_max(x[q].x);
+        w[q] = ex2(x[q].x - mx[q]);
+        ls[q] = fmaf(w[q], x[q].y, ls[q]);
+        zs[q] = fmaf(w[q], x[q].z, zs[q]);
+      }
+      const int n = min(32, parts - k0);
+#pragma unroll 1
+      for (int i = 0; i < n; i += CH) {
+        float4 v[CH][NQ];
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+            v[j][q] = i + j < n && q < nq ? __ldcg(reinterpret_cast<const float4*>(part(k0 + i + j, q) + 4) + lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const float wj = __shfl_sync(kFull, w[q], (i + j) & 31);
+            acc[q][0] = fmaf(wj, v[j][q].x, acc[q][0]);
+            acc[q][1] = fmaf(wj, v[j][q].y, acc[q][1]);
+            acc[q][2] = fmaf(wj, v[j][q].z, acc[q][2]);
+            acc[q][3] = fmaf(wj, v[j][q].w, acc[q][3]);
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const float l1 = warp_sum(ls[q]), z1 = warp_sum(zs[q]), inv = l1 == 0.f ? 0.f : 1.f / l1;
+      if (q < nq)
+        *reinterpret_cast<uint2*>(out + q * kHeadDim + 4 * lane) =
+            make_uint2(pack_h2((acc[q][0] + z1) * inv, (acc[q][1] + z1) * inv), pack_h2((acc[q][2] + z1) * inv, (acc[q][3] + z1) * inv));
+    }
+    if (lane == 0) a.tickets[static_cast<size_t>(s) * a.heads * a.passes + e] = 0;
+  }
+
+  __device__ __forceinline__ void run(long long w, long long nw, long long all, int seq0, long long rem) {
+    Core& core = static_cast<Core&>(*this);
+    worker = w;
+    workers = nw;
+    total = all;
+    const long long f0 = total * w / workers;
+    int left = static_cast<int>(total * (w + 1) / workers - f0);  // below 2^31: rows * units a head are
+    {
+      bool bad;
+      const int n = units_of<UT>(span_of(a, seq0, &bad)).total, he = static_cast<int>(rem / n);
+      take(enter<UT>(a, S.cur, seq0, he, static_cast<int>(rem - static_cast<long long>(he) * n), true));
+      steps_ = 0;
+      slot = 0;
+      head = true;
+    }
+    fetch();
+    issue_k(true);
+    issue_v(true);
+    uint32_t kp = 0, vp = 0;
+    load_pairs(kp, vp);
+    struct Head {
+      int seq, he, units;
+      long long f0;
+    } pend[2];
+    int npend = 0;
+    long long at = f0;
+    while (left > 0) {
+      const Cursor& c = S.cur;
+      const int s = c.seq, e = c.he, l0 = c.local, units = c.un.total;
+      const int count = min(left, units - l0), nq = min(count, max(0, c.un.q_units - l0));
+      __syncwarp();
+      if (lane == 0) S.now = c;
+      __syncwarp();
+      slot_now = slot;
+      full_from = (S.now.sp.start + UT - 1) / UT;
+      sink_full = S.now.sp.sink_end / UT;
+      copies_wait<1>();  // the head's queries are here with its first K half
+      core.start_head();
+      // K of the unit in hand, then V; the next unit's K is copied behind the one, its V behind the other
+#pragma unroll 1
+      for (int i = 0; i < nq; ++i) {
+        const int ux = x;
+        const bool good = ok, more = --left > 0;
+        const uint32_t ckp = kp, cvp = vp;
+        if (more) {
+          advance();
+          fetch();
+        }
+        copies_wait<1>();
+        if (good) core.quant_k(ux, ckp, cvp);
+        __syncwarp();  // the K half has been read, and the P operands are written
+        issue_k(more);
+        if (more) load_pairs(kp, vp);
+        copies_wait<1>();
+        if (good) core.quant_v();
+        __syncwarp();
+        issue_v(more);
+      }
+      if (count > nq) {
+        typename Core::Res r;
+        core.res_start(r);
+#pragma unroll 1
+        for (int i = nq; i < count; ++i) {
+          const int ux = x;
+          const bool good = ok, more = --left > 0;
+          if (more) {
+            advance();
+            fetch();
+          }
+          copies_wait<1>();
+          if (good) core.res_k(ux, r);
+          __syncwarp();
+          issue_k(more);
+          if (more) load_pairs(kp, vp);
+          copies_wait<1>();
+          if (good) core.res_v(r);
+          __syncwarp();
+          issue_v(more);
+        }
+        core.res_end(r);
+      }
+      const bool whole = count == units;
+      core.finish(whole, at == f0 ? 0 : 1);
+      if (!whole) {
+        pend[npend].seq = s;
+        pend[npend].he = e;
+        pend[npend].units = units;
+        pend[npend].f0 = at - l0;
+        ++npend;
+      }
+      at += count;
+    }
+    if (npend == 0) return;
+    // one fence publishes this warp's partials before its tickets; the last part of a head joins it
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) {
+      for (int i = 0; i < npend; ++i) {
+        const int others = static_cast<int>(worker_of(pend[i].f0 + pend[i].units - 1, workers, total) - worker_of(pend[i].f0, workers, total));
+        if (atomicAdd(a.tickets + static_cast<size_t>(pend[i].seq) * a.heads * a.passes + pend[i].he, 1) == others) last |= 1 << i;
+      }
+      if (last) __threadfence();
+    }
+    last = __shfl_sync(kFull, last, 0);
+    if (!last) return;
+    __threadfence();
+#pragma unroll 1
+    for (int i = 0; i < npend; ++i)
+      if ((last >> i) & 1) merge(a, pend[i].seq, pend[i].he, pend[i].units, pend[i].f0, workers, total);
+  }
+};
+
+// Several queries per KV head: fp16 products, two columns per query (top of the file).
+template <int BITS, int NB>
+struct Many : Walker<BITS, NB, Many<BITS, NB>> {
+  using Base = Walker<BITS, NB, Many<BITS, NB>>;
+  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full, Base::worker;
+  using Base::UT, Base::PT, Base::P, Base::NQ, Base::seen;
+  static constexpr int HP = P / 2;                  // code pairs per word
+  static constexpr int MT = UT / 16;                // K tiles per unit
+  static constexpr int KW = kHeadDim / P / 4;       // K words per lane and token
+  struct Res {
+    float p[NB][2], r[NB][8][4];
+  };
+
+  // state of the head in hand: lane (g, t) is query t (of each column block) and channels 16 g .. 16 g + 15.
+  // Weights are 2^(logit - m): m is the largest logit when it was last raised, by at most kSlack below the largest.
+  float m[NB], thr[NB], l[NB], Z[NB], o[NB][8][4];
+  float qs[NB][4];   // scale * log2 e * sum of q over channels 32 i .. 32 i + 31
+  int qe[NB];        // exponent of the largest |q|
+  int eref;          // exponent field of the largest V scale so far: o carries 2^-eref (P operands 2^(24 - eref))
+
+  using Base::Base;
+
   // ---- the head's queries ----------------------------------------------------------------------------
   __device__ void start_head() {
-    const int he = S.cur.he_now, h = he / a.passes, pass = he - h * a.passes;
-    bool bad = false;
-    const int row = q_row(a, S.cur.seq_now, &bad);
-    const int q0 = pass * a.per_pass, nq = min(a.per_pass, a.gqa - q0);
-    const uint16_t* base = a.q + (static_cast<size_t>(row) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0) * kHeadDim;
-    __syncwarp();  // the previous head's raw queries are no longer read
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int qi = 4 * b + (g >> 1);
       uint4 v[4];
+      const uint4* src = reinterpret_cast<const uint4*>(S.q[slot_now] + (4 * b + (g >> 1)) * kQRow + 64 * t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = qi < nq ? __ldg(reinterpret_cast<const uint4*>(base + static_cast<size_t>(qi) * kHeadDim + 32 * t) + i)
-                       : make_uint4(0, 0, 0, 0);
-      if ((g & 1) == 0) {
-        uint4* dst = reinterpret_cast<uint4*>(S.q[b] + (g >> 1) * kQRow + 64 * t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = v[i];
-      }
+      for (int i = 0; i < 4; ++i) v[i] = src[i];
       float f[32], big = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -479,7 +714,7 @@ struct Attender {
     const bool full = ux >= full_from || ux < sink_full;
     if (!full) {  // V pieces that are hidden whole have no say (their s and z may be anything)
       const int p0 = tok0 + PT * t;
-      if (p0 >= S.cur.now.sink_end && p0 + PT <= S.cur.now.start) vp = 0;
+      if (p0 >= S.now.sp.sink_end && p0 + PT <= S.now.sp.start) vp = 0;
     }
     const unsigned ksm = __reduce_max_sync(kFull, kp & 0xFFFFu), vsm = __reduce_max_sync(kFull, vp & 0xFFFFu);
     const int ek = max(1, static_cast<int>(ksm >> 10)), ev = max(1, static_cast<int>(vsm >> 10));
@@ -560,7 +795,7 @@ struct Attender {
                                   : tok0 + 16 * (tt0 + (i >> 1)) + 8 * (i & 1) + jl;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (!seen(tok + HP * y))
+          if (!seen(S.now.sp, tok + HP * y))
 #pragma unroll
             for (int b = 0; b < NB; ++b) lg[b][i][y] = -INFINITY;
       }
@@ -696,7 +931,15 @@ struct Attender {
 
   // ---- residual units, on the tensor cores too: K rows with the raw queries, V rows transposed on the way ----------
   // Logits of rows g and g + 8 for query t, as weights times 2^10 in p.
-  __device__ __forceinline__ void res_k(int ux, float (&p)[NB][2], float (&r)[NB][8][4]) {
+  __device__ __forceinline__ void res_start(Res& s) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v8 = 0; v8 < 8; ++v8) s.r[b][v8][0] = s.r[b][v8][1] = s.r[b][v8][2] = s.r[b][v8][3] = 0.f;
+  }
+  __device__ __forceinline__ void res_k(int ux, Res& s) {
+    float(&p)[NB][2] = s.p;
+    float(&r)[NB][8][4] = s.r;
     float c[NB][4];
     const uint32_t row = smem_u32(S.k) + (lane & 15) * kRow + (lane >> 4) * 16;
 #pragma unroll
@@ -705,7 +948,7 @@ struct Attender {
       ldmatrix4(x, row + 32 * i);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(S.q[b] + (g >> 1) * kQRow) + 8 * i + t;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(S.q[slot_now] + (4 * b + (g >> 1)) * kQRow) + 8 * i + t;
         const uint32_t b0 = (g & 1) ? 0u : q[0], b1 = (g & 1) ? 0u : q[4];
         if (i == 0)
           mma16_first(c[b], x[0], x[1], x[2], x[3], b0, b1);
@@ -713,8 +956,8 @@ struct Attender {
           mma16(c[b], x[0], x[1], x[2], x[3], b0, b1);
       }
     }
-    const int tok0 = S.cur.now.quant + ux * kResTokens;
-    const bool s0 = seen(tok0 + g), s1 = seen(tok0 + g + 8);
+    const int tok0 = S.now.sp.quant + ux * kResTokens;
+    const bool s0 = seen(S.now.sp, tok0 + g), s1 = seen(S.now.sp, tok0 + g + 8);
     bool above = false;
     float mu[NB];
 #pragma unroll
@@ -746,14 +989,9 @@ struct Attender {
     }
   }
   // r: tile v8 holds channels 16 v8 + g (row g) and 16 v8 + 8 + g (row g + 8), columns as o; times 2^10.
-  __device__ __forceinline__ void res_v(int ux, const float (&p)[NB][2], float (&r)[NB][8][4]) {
-    const int tok0 = S.cur.now.quant + ux * kResTokens;
-    if (tok0 < S.cur.now.start || tok0 + kResTokens > S.cur.now.len) {  // hidden rows may hold anything: clear them
-#pragma unroll 1
-      for (int j = 0; j < kResTokens; ++j)
-        if (!seen(tok0 + j)) *reinterpret_cast<uint2*>(S.v + j * kRow + 8 * lane) = make_uint2(0, 0);
-      __syncwarp();
-    }
+  __device__ __forceinline__ void res_v(Res& s) {
+    const float(&p)[NB][2] = s.p;
+    float(&r)[NB][8][4] = s.r;
     uint32_t pb[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -777,7 +1015,8 @@ struct Attender {
     }
   }
   // The residual rows' share of the output, through shared memory to the layout of o.
-  __device__ __forceinline__ void add_residual(const float (&r)[NB][8][4]) {
+  __device__ __forceinline__ void res_end(Res& s) {
+    const float(&r)[NB][8][4] = s.r;
     float* buf = reinterpret_cast<float*>(S.p[0]);  // 4 queries at a time of 64 channels: 1 KB
     const float f = pow2i(-10 - eref);
 #pragma unroll
@@ -808,10 +1047,7 @@ struct Attender {
   // ---- the end of a head's segment -----------------------------------------------------------------------
   // Lane (g, t): o of query t (each column block), channels 16 g .. 16 g + 15.
   __device__ void finish(bool whole, int slot) {
-    const int he = S.cur.he_now, h = he / a.passes, pass = he - h * a.passes;
-    const int q0 = pass * a.per_pass, nq = min(a.per_pass, a.gqa - q0);
-    bool bad = false;
-    const int row = q_row(a, S.cur.seq_now, &bad);
+    const int nq = S.now.queries;
     const float back = pow2i(eref);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -835,7 +1071,7 @@ struct Attender {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = pack_h2((f[2 * i] + zs) * inv, (f[2 * i + 1] + zs) * inv);
         uint4* dst = reinterpret_cast<uint4*>(
-            a.out + (static_cast<size_t>(row) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0 + qi) * kHeadDim + 16 * g);
+            a.out + (static_cast<size_t>(S.now.row) * a.heads * a.gqa + S.now.q0 + qi) * kHeadDim + 16 * g);
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
@@ -847,184 +1083,352 @@ struct Attender {
       }
     }
   }
+};
 
-  // Worker whose range holds unit f: ranges start at floor(total w / workers).
-  __device__ __forceinline__ long long worker_of(long long f) const { return ((f + 1) * workers + total - 1) / total - 1; }
+// ---- one query per KV head: exact integer products of code bytes and byte digits -----------------------------------------
+// With one query the columns of the fp16 scheme stay mostly empty, and its masks (nine per 2-bit word) set the time.  Here the
+// A operand of mma m16n8k32 (u8 x s8, int32 sums) takes a code word as it is and its copies without the lowest codes of each
+// byte: V_k = sum over i >= k of c_i 2^(b i), k = 0 .. P / 4 - 1, one AND per copy but the first.  Against
+// X_k = W (Q_k 2^(-b k) - Q_(k-1) 2^(-b (k-1))), W = 2^(b (P / 4 - 1)), the products add up to W sum c_k Q_k, exactly.  Q is
+// q_c s_g(c), P is p_t s_g(t), as fixed point relative to the largest of the block (23 bits) or to its bound (24 bits); each X
+// (below 2^30) is four signed byte digits, one B column each.  Two tiles of 16 tokens (or channels) share a sum: the digits of
+// the one sit in columns 0..3, of the other in columns 4..7, each against zeros for the other tile.
+constexpr float kQFixed = 8388544.f;   // 2^23 - 64
+constexpr float kPFixed = 16777088.f;  // 2^24 - 128
 
-  // The workers that hold a part of a head left one partial each: the first of them in its slot 1
-  // unless its range starts with the head, the others in their slot 0.
-  __device__ void merge(int s, int e, long long f0, int units) {
-    const long long w0 = worker_of(f0), w1 = worker_of(f0 + units - 1);
-    const int parts = static_cast<int>(w1 - w0 + 1);
-    const int slot0 = total * w0 / workers >= f0 ? 0 : 1;
-    const int h = e / a.passes, pass = e - h * a.passes;
-    const int q0 = pass * a.per_pass, nq = min(a.per_pass, a.gqa - q0);
-    bool bad = false;
-    const int row = q_row(a, s, &bad);
-#pragma unroll 1
-    for (int qi = 0; qi < nq; ++qi) {
-      auto part = [&](int k) { return a.partials + (((w0 + k) * 2 + (k == 0 ? slot0 : 0)) * NQ + qi) * kPart; };
-      float mx = kNoMax;
-      for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, __ldcg(part(k)));
+__device__ __forceinline__ void mma_bytes(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float max_of_warp(float v) {  // one instruction; NaN is ignored
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int BITS>
+struct One : Walker<BITS, 0, One<BITS>> {
+  using Base = Walker<BITS, 0, One<BITS>>;
+  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full, Base::worker;
+  using Base::UT, Base::PT, Base::P, Base::seen;
+  static constexpr int NV = P / 4;            // copies of a word: 4 at 2 bits, 2 at 4 bits
+  static constexpr int W = 1 << (BITS * (NV - 1));
+  static constexpr int TJ = UT / 32;          // tokens per lane and unit
+  struct Res {
+    float p[2], r[8][4];
+  };
+
+  // Lane holds the queries of the channels whose digits it forms: P word + NV m + k, word = lane / NV, k = lane % NV, m = 0..3
+  // (K piece lane / 8), and channels 4 lane .. 4 lane + 3 of the output; l and Z are this lane's share.
+  float q[4], qsum, m, l, Z, o[4];
+  float alpha, invv;
+
+  using Base::Base;
+
+  __device__ __forceinline__ void start_head() {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(S.q[slot_now]) + P * (lane / NV) + (lane % NV);
+    qsum = 0.f;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-      float ls = 0.f, zs = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k0 = 0; k0 < parts; k0 += 32) {
-        float w = 0.f;
-        if (k0 + lane < parts) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(part(k0 + lane)));
-          w = ex2(x.x - mx);
-          ls = fmaf(w, x.y, ls);
-          zs = fmaf(w, x.z, zs);
-        }
-        const int n = min(32, parts - k0);
-        for (int i = 0; i < n; i += 16) {
-          float4 v[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            v[j] = i + j < n ? __ldcg(reinterpret_cast<const float4*>(part(k0 + i + j) + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float wj = __shfl_sync(kFull, w, (i + j) & 31);
-            acc[0] = fmaf(wj, v[j].x, acc[0]);
-            acc[1] = fmaf(wj, v[j].y, acc[1]);
-            acc[2] = fmaf(wj, v[j].z, acc[2]);
-            acc[3] = fmaf(wj, v[j].w, acc[3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        ls += __shfl_xor_sync(kFull, ls, off);
-        zs += __shfl_xor_sync(kFull, zs, off);
-      }
-      const float inv = ls == 0.f ? 0.f : 1.f / ls;
-      *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(row) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + q0 + qi) * kHeadDim +
-                                4 * lane) =
-          make_uint2(pack_h2((acc[0] + zs) * inv, (acc[1] + zs) * inv), pack_h2((acc[2] + zs) * inv, (acc[3] + zs) * inv));
+    for (int i = 0; i < 4; ++i) {
+      q[i] = h2f(src[NV * i]) * a.qscale;
+      qsum += q[i];
     }
-    if (lane == 0) a.tickets[static_cast<size_t>(s) * a.heads * a.passes + e] = 0;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) qsum += __shfl_xor_sync(kFull, qsum, off);  // of the piece's 32 channels
+    m = kNoMax;
+    l = Z = o[0] = o[1] = o[2] = o[3] = 0.f;
+    if (lane == 0) S.zero4 = make_uint4(0, 0, 0, 0);
+    __syncwarp();
   }
 
-  __device__ void run(long long w, long long nw, long long all, int seq0, long long rem) {
-    worker = w;
-    workers = nw;
-    total = all;
-    const long long f0 = total * w / workers;
-    int left = static_cast<int>(total * (w + 1) / workers - f0);  // below 2^31: rows * units a head are
+  // Digits of four values: digit d of x[i] in byte i of word d, from the bytes of x + 0x80808080, each less 128.
+  __device__ static __forceinline__ void digits(const int (&x)[4], uint32_t (&wd)[4]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = static_cast<uint32_t>(x[i]) + 0x80808080u;
+    const uint32_t t0 = __byte_perm(u[0], u[1], 0x5140), t1 = __byte_perm(u[0], u[1], 0x7362);
+    const uint32_t t2 = __byte_perm(u[2], u[3], 0x5140), t3 = __byte_perm(u[2], u[3], 0x7362);
+    wd[0] = __byte_perm(t0, t2, 0x5410) ^ 0x80808080u;
+    wd[1] = __byte_perm(t0, t2, 0x7632) ^ 0x80808080u;
+    wd[2] = __byte_perm(t1, t3, 0x5410) ^ 0x80808080u;
+    wd[3] = __byte_perm(t1, t3, 0x7632) ^ 0x80808080u;
+  }
+  // Operand words of code word i (a K word, or a V word row), copy k and column c (digit 3 - c): a lane t of the products
+  // reads those of words NK t .. NK t + NK - 1 as 16-byte vectors; the XOR puts its four lanes t in four bank groups.
+  __device__ static __forceinline__ uint32_t* operand(uint4* rows, int row, int c) {
+    return reinterpret_cast<uint32_t*>(rows) + 16 * row + 4 * (c ^ ((row >> 1) & 3));
+  }
+  // Two digit columns of a tile end in each lane; the partner lane has the other two.  Even lanes t keep row g, odd lanes
+  // row g + 8, whole (every digit sum is below 2^22).
+  __device__ __forceinline__ float gather(const int (&c)[4]) const {
+    const bool odd = t & 1;
+    const float sc = odd ? 1.f : 65536.f;
+    const float fg = static_cast<float>(c[0] * 256 + c[1]) * sc, fh = static_cast<float>(c[2] * 256 + c[3]) * sc;
+    return (odd ? fh : fg) + __shfl_xor_sync(kFull, odd ? fg : fh, 1);
+  }
+  // Copies of the words of rows g and g + 8 against the operands of one word: W sum c Q of both rows.
+  __device__ static __forceinline__ void products(int (&c)[4], uint32_t wg, uint32_t wh, const uint4& b, int half) {
+    if constexpr (BITS == 2) {
+      mma_bytes(c, wg, wh, wg & 0xFCFCFCFCu, wh & 0xFCFCFCFCu, b.x, b.y);
+      mma_bytes(c, wg & 0xF0F0F0F0u, wh & 0xF0F0F0F0u, wg & 0xC0C0C0C0u, wh & 0xC0C0C0C0u, b.z, b.w);
+    } else {
+      mma_bytes(c, wg, wh, wg & 0xF0F0F0F0u, wh & 0xF0F0F0F0u, half ? b.z : b.x, half ? b.w : b.y);
+    }
+  }
+
+  __device__ __forceinline__ void quant_k(int ux, uint32_t kp, uint32_t vp) {
+    const bool full = ux >= full_from || ux < sink_full;
+    const int tok0 = ux * UT;
+    if (!full) {  // V pieces that are hidden whole have no say (their s and z may be anything)
+      const int p0 = tok0 + PT * t;
+      if (p0 >= S.now.sp.sink_end && p0 + PT <= S.now.sp.start) vp = 0;
+    }
+    // Q operands of the block
+    const uint32_t kq = __shfl_sync(kFull, kp, lane >> 3);
+    const float s = h2f(static_cast<uint16_t>(kq));
+    float big = 0.f, cst = h2f(static_cast<uint16_t>(kq >> 16)) * qsum, v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = q[i] * s;
+      big = fmaxf(big, fabsf(v[i]));
+    }
+    big = max_of_warp(big);
+    cst += __shfl_xor_sync(kFull, cst, 8);
+    cst += __shfl_xor_sync(kFull, cst, 16);
+    const float fix = big > 0.f ? kQFixed * reciprocal(big) : 0.f, inv = big * (1.0f / (W * kQFixed));
     {
-      bool bad;
-      const int n = units_of<UT>(span_of(a, seq0, &bad)).total, he = static_cast<int>(rem / n);
-      take(enter<UT>(a, S.cur, seq0, he, static_cast<int>(rem - static_cast<long long>(he) * n), true));
-      steps_ = 0;
-    }
-    fetch();
-    issue_k(true);
-    issue_v(true);
-    uint32_t kp = 0, vp = 0;
-    load_pairs(kp, vp);
-    struct Head {
-      int seq, he, units;
-      long long f0;
-    } pend[2];
-    int npend = 0;
-    long long at = f0;
-    while (left > 0) {
-      Cursor& c = S.cur;
-      const int s = c.seq, e = c.he, l0 = c.local, units = c.un.total;
-      const int count = min(left, units - l0), nq = min(count, max(0, c.un.q_units - l0));
-      __syncwarp();
-      if (lane == 0) {
-        c.now = c.sp;
-        c.he_now = e;
-        c.seq_now = s;
-      }
-      __syncwarp();
-      full_from = (c.now.start + UT - 1) / UT;
-      sink_full = c.now.sink_end / UT;
-      start_head();
-      // K of the unit in hand, then V; the next unit's K is copied behind the one, its V behind the other
-#pragma unroll 1
-      for (int i = 0; i < nq; ++i) {
-        const int ux = x;
-        const bool good = ok, more = --left > 0;
-        const uint32_t ckp = kp, cvp = vp;
-        if (more) {
-          advance();
-          fetch();
-        }
-        copies_wait<1>();
-        if (good) quant_k(ux, ckp, cvp);
-        __syncwarp();  // the K half has been read, and the P operands are written
-        issue_k(more);
-        if (more) load_pairs(kp, vp);
-        copies_wait<1>();
-        if (good) quant_v();
-        __syncwarp();
-        issue_v(more);
-      }
-      if (count > nq) {
-        float r[NB][8][4];
+      const int k = lane % NV, xa = W >> (BITS * k), xb = k ? (W << BITS) >> (BITS * k) : 0;
+      int xs[4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const int Q = __float2int_rn(v[i] * fix), below = __shfl_up_sync(kFull, Q, 1);
+        xs[i] = Q * xa - below * xb;
+      }
+      uint32_t wd[4];
+      digits(xs, wd);
 #pragma unroll
-          for (int v8 = 0; v8 < 8; ++v8) r[b][v8][0] = r[b][v8][1] = r[b][v8][2] = r[b][v8][3] = 0.f;
-#pragma unroll 1
-        for (int i = nq; i < count; ++i) {
-          const int ux = x;
-          const bool good = ok, more = --left > 0;
-          if (more) {
-            advance();
-            fetch();
-          }
-          float p[NB][2];
-          copies_wait<1>();
-          if (good) res_k(ux, p, r);
-          __syncwarp();
-          issue_k(more);
-          if (more) load_pairs(kp, vp);
-          copies_wait<1>();
-          if (good) res_v(ux, p, r);
-          __syncwarp();
-          issue_v(more);
-        }
-        add_residual(r);
-      }
-      const bool whole = count == units;
-      finish(whole, at == f0 ? 0 : 1);
-      if (!whole) {
-        pend[npend].seq = s;
-        pend[npend].he = e;
-        pend[npend].units = units;
-        pend[npend].f0 = at - l0;
-        ++npend;
-      }
-      at += count;
+      for (int c = 0; c < 4; ++c) operand(S.qh[0][0], lane >> 2, c)[lane & 3] = wd[3 - c];
     }
-    if (npend == 0) return;
-    // one fence publishes this warp's partials before its tickets; the last part of a head joins it
-    __threadfence();
     __syncwarp();
-    int last = 0;
-    if (lane == 0) {
-      for (int i = 0; i < npend; ++i) {
-        const int others = static_cast<int>(worker_of(pend[i].f0 + pend[i].units - 1) - worker_of(pend[i].f0));
-        if (atomicAdd(a.tickets + static_cast<size_t>(pend[i].seq) * a.heads * a.passes + pend[i].he, 1) == others) last |= 1 << i;
+    // logits: pair j, tile b holds on row g + 8 c token P r + NV j' .. of word row r = g / 4 + 2 c + 4 b, so that after the
+    // exchange lane (g, t) has tokens of word row g / 4 + 2 (t % 2) + 4 (t / 2): those whose P digits it forms
+    float lg[TJ];
+    {
+      const int si = 8 * t + ((g & 3) ^ t);
+      const uint4 *pe = g < 4 ? &S.qh[0][0][si] : &S.zero4, *po = g >= 4 ? &S.qh[0][0][si] : &S.zero4;
+      const uint4 be[2] = {pe[0], pe[g < 4 ? 4 : 0]}, bo[2] = {po[0], po[g >= 4 ? 4 : 0]};
+      const uint8_t* kt = BITS == 2 ? S.k + (16 * (g >> 2) + (g & 3)) * 32 + 8 * t
+                                    : S.k + (8 * (g >> 2) + 4 * ((g >> 1) & 1) + (g & 1)) * 64 + 16 * t;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        int c[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint8_t* r0 = kt + 128 * j + 2048 * b;
+          const uint4& B0 = b ? bo[0] : be[0];
+          const uint4& B1 = b ? bo[1] : be[1];
+          if constexpr (BITS == 2) {
+            const uint2 wg = *reinterpret_cast<const uint2*>(r0), wh = *reinterpret_cast<const uint2*>(r0 + 1024);
+            products(c, wg.x, wh.x, B0, 0);
+            products(c, wg.y, wh.y, B1, 0);
+          } else {
+            const uint4 wg = *reinterpret_cast<const uint4*>(r0), wh = *reinterpret_cast<const uint4*>(r0 + 1024);
+            products(c, wg.x, wh.x, B0, 0);
+            products(c, wg.y, wh.y, B0, 1);
+            products(c, wg.z, wh.z, B1, 0);
+            products(c, wg.w, wh.w, B1, 1);
+          }
+        }
+        lg[j] = fmaf(gather(c), inv, cst);
       }
-      if (last) __threadfence();
     }
-    last = __shfl_sync(kFull, last, 0);
-    if (!last) return;
-    __threadfence();
-#pragma unroll 1
-    for (int i = 0; i < npend; ++i)
-      if ((last >> i) & 1) merge(pend[i].seq, pend[i].he, pend[i].f0, pend[i].units);
+    const int r = (g >> 2) + 2 * (t & 1) + 4 * (t >> 1);
+    const int k = BITS == 2 ? g & 3 : g & 1, in = BITS == 2 ? k : 4 * ((g >> 1) & 1) + k;  // first token within the row
+    if (!full) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        if (!seen(S.now.sp, tok0 + P * r + in + NV * j)) lg[j] = -INFINITY;
+    }
+    // softmax, and P operands relative to the unit's largest weight times its largest s
+    float mu = lg[0];
+#pragma unroll
+    for (int j = 1; j < TJ; ++j) mu = fmaxf(mu, lg[j]);
+    mu = max_of_warp(mu);
+    const float smax = max_of_warp(h2f(static_cast<uint16_t>(vp)));
+    const uint32_t vq = __shfl_sync(kFull, vp, r >> 1);
+    const float mn = fmaxf(m, mu), d = mu - mn;  // d <= 0: the unit's largest weight is 2^d
+    alpha = ex2(m - mn);
+    m = mn;
+    const bool some = d > -64.f && smax > 0.f;
+    const float f = some ? kPFixed * reciprocal(smax) * ex2(-d) * h2f(static_cast<uint16_t>(vq)) : 0.f;
+    invv = some ? ex2(d) * smax * (1.0f / (W * kPFixed)) : 0.f;
+    const int xa = W >> (BITS * k), xb = k ? (W << BITS) >> (BITS * k) : 0;
+    float ps = 0.f;
+    int xs[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const float p = ex2(lg[j] - mn);
+      ps += p;
+      const int Pf = static_cast<int>(__float2uint_rn(p * f)), below = __shfl_up_sync(kFull, Pf, 4);
+      xs[j] = Pf * xa - below * xb;
+    }
+    l = fmaf(l, alpha, ps);
+    Z = fmaf(Z, alpha, ps * h2f(static_cast<uint16_t>(vq >> 16)));
+    uint32_t wd[4];
+    digits(xs, wd);
+    if constexpr (BITS == 2) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) operand(S.p[0], r, c)[k] = wd[3 - c];
+    } else {  // bytes 2 mu and 2 mu + 1 of the words of row r, copy k: row pairs are the vectors
+      const int mu2 = (g >> 1) & 1;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        reinterpret_cast<uint16_t*>(reinterpret_cast<uint32_t*>(S.p[0]) + 16 * (r >> 1) + 4 * (c ^ (r >> 1)) + 2 * (r & 1) + k)[mu2] =
+            static_cast<uint16_t>(wd[3 - c]);
+    }
+  }
+
+  // Pair v: tile b holds on row g + 8 c channel 16 g + 8 b + 4 c + v; lane (g, t) reads V word rows 2 t and 2 t + 1.
+  __device__ __forceinline__ void quant_v() {
+    uint4 be[2], bo[2];
+    if constexpr (BITS == 2) {
+      const int si = 8 * t + ((g & 3) ^ t);
+      const uint4 *pe = g < 4 ? &S.p[0][si] : &S.zero4, *po = g >= 4 ? &S.p[0][si] : &S.zero4;
+      be[0] = pe[0], be[1] = pe[g < 4 ? 4 : 0], bo[0] = po[0], bo[1] = po[g >= 4 ? 4 : 0];
+    } else {
+      const uint4 x = S.p[0][4 * t + ((g & 3) ^ t)], none = make_uint4(0, 0, 0, 0);
+      be[0] = be[1] = g < 4 ? x : none;
+      bo[0] = bo[1] = g >= 4 ? x : none;
+    }
+    int c[4][4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) c[v][0] = c[v][1] = c[v][2] = c[v][3] = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* row = S.v + t * kVPieceStride + x * 512 + 64 * g;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(row + 32 * b), hi = *reinterpret_cast<const uint4*>(row + 32 * b + 16);
+        const uint4& B = b ? bo[x] : be[x];
+        products(c[0], lo.x, hi.x, B, x);
+        products(c[1], lo.y, hi.y, B, x);
+        products(c[2], lo.z, hi.z, B, x);
+        products(c[3], lo.w, hi.w, B, x);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = fmaf(o[v], alpha, gather(c[v]) * invv);
+  }
+
+  // ---- residual rows: fp16 products as for several queries, every column the one query --------------------------------
+  __device__ __forceinline__ void res_start(Res& s) const {
+#pragma unroll
+    for (int v8 = 0; v8 < 8; ++v8) s.r[v8][0] = s.r[v8][1] = s.r[v8][2] = s.r[v8][3] = 0.f;
+  }
+  __device__ __forceinline__ void res_k(int ux, Res& s) {
+    float c[4];
+    const uint32_t row = smem_u32(S.k) + (lane & 15) * kRow + (lane >> 4) * 16;
+    const uint32_t* qw = reinterpret_cast<const uint32_t*>(S.q[slot_now]) + t;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t x[4];
+      ldmatrix4(x, row + 32 * i);
+      if (i == 0)
+        mma16_first(c, x[0], x[1], x[2], x[3], qw[0], qw[4]);
+      else
+        mma16(c, x[0], x[1], x[2], x[3], qw[8 * i], qw[8 * i + 4]);
+    }
+    const int tok0 = S.now.sp.quant + ux * kResTokens;
+    const float l0 = seen(S.now.sp, tok0 + g) ? c[0] * a.qscale : -INFINITY;
+    const float l1 = seen(S.now.sp, tok0 + g + 8) ? c[2] * a.qscale : -INFINITY;
+    const float mn = fmaxf(m, max_of_warp(fmaxf(l0, l1)));
+    if (mn > m) {  // the same for every lane
+      const float al = ex2(m - mn);
+      m = mn;
+      l *= al;
+      Z *= al;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] *= al;
+#pragma unroll
+      for (int v8 = 0; v8 < 8; ++v8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.r[v8][i] *= al;
+    }
+    const float p0 = ex2(l0 - mn), p1 = ex2(l1 - mn);
+    if (t == 0) l += p0 + p1;  // lanes t hold the same rows
+    s.p[0] = p0 * 1024.f;
+    s.p[1] = p1 * 1024.f;
+  }
+  __device__ __forceinline__ void res_v(Res& s) {
+    uint32_t pb[2];
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __shfl_sync(kFull, s.p[i >> 1], 4 * (2 * t + (i & 1)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t hi = pack_h2(x[2 * i], x[2 * i + 1]);
+      const float2 f = unpack_h2(hi);
+      pb[i] = (g & 1) ? pack_h2(x[2 * i] - f.x, x[2 * i + 1] - f.y) : hi;
+    }
+    const uint32_t row = smem_u32(S.v) + ((lane & 7) + (lane >> 4) * 8) * kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll
+    for (int v8 = 0; v8 < 8; ++v8) {
+      uint32_t w[4];
+      ldmatrix4_trans(w, row + 32 * v8);
+      mma16(s.r[v8], w[0], w[1], w[2], w[3], pb[0], pb[1]);
+    }
+  }
+  __device__ __forceinline__ void res_end(Res& s) {
+    float* buf = reinterpret_cast<float*>(S.p[0]);  // 128 channels
+    __syncwarp();
+    if (t == 0) {
+#pragma unroll
+      for (int v8 = 0; v8 < 8; ++v8) {
+        buf[16 * v8 + g] = (s.r[v8][0] + s.r[v8][1]) * (1.f / 1024.f);
+        buf[16 * v8 + 8 + g] = (s.r[v8][2] + s.r[v8][3]) * (1.f / 1024.f);
+      }
+    }
+    __syncwarp();
+    const float4 x = *reinterpret_cast<const float4*>(buf + 4 * lane);
+    o[0] += x.x;
+    o[1] += x.y;
+    o[2] += x.z;
+    o[3] += x.w;
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void finish(bool whole, int slot) {
+    const float ls = warp_sum(l), zs = warp_sum(Z);
+    if (whole) {
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(S.now.row) * a.heads * a.gqa + S.now.q0) * kHeadDim + 4 * lane) =
+          make_uint2(pack_h2((o[0] + zs) * inv, (o[1] + zs) * inv), pack_h2((o[2] + zs) * inv, (o[3] + zs) * inv));
+    } else {
+      float* dst = a.partials + (worker * 2 + slot) * kPart;
+      if (lane == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m, ls, zs, 0.f);
+      *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
+    }
   }
 };
 
 template <int BITS, int NB>
+struct CoreOf {
+  using type = Many<BITS, NB>;
+};
+template <int BITS>
+struct CoreOf<BITS, 0> {
+  using type = One<BITS>;
+};
+
+template <int BITS, int NB>
 __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int W = attend_warps<NB>(), T = W * 32, UT = Attender<BITS, NB>::UT;
+  constexpr int W = attend_warps<NB>(), T = W * 32, UT = CoreOf<BITS, NB>::type::UT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = WarpSmem<BITS, NB>;
   __shared__ int warp_sum[W], cum[T + 1];  // units per head before each thread's rows
@@ -1069,7 +1473,7 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   }
   int row = lo * per, first = cum[lo];
   for (int n; first + (n = row_units<UT>(a, row)) <= want; ++row) first += n;
-  Attender<BITS, NB> d(a, reinterpret_cast<Smem*>(smem_raw)[warp], lane);
+  typename CoreOf<BITS, NB>::type d(a, reinterpret_cast<Smem*>(smem_raw)[warp], lane);
   d.run(worker, workers, total, row, f0 - first * he_count);
 }
 
@@ -1085,15 +1489,17 @@ cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
 }
 
 struct Shape {
-  int passes, per_pass, blocks;  // query passes per KV head, queries of a pass, column blocks of four queries
+  int passes, per_pass, blocks;  // query passes per KV head, queries of a pass, column blocks of four (0: one query)
+  int warps;                     // per CTA
   long long workers;             // at most
 };
 Shape shape_of(long long rows, int heads, int gqa, long long max_units) {
   Shape s;
   s.passes = (gqa + 7) / 8;
   s.per_pass = (gqa + s.passes - 1) / s.passes;
-  s.blocks = s.per_pass > 4 ? 2 : 1;
-  const long long warps = static_cast<long long>(kMaxCtas) * (s.blocks == 1 ? attend_warps<1>() : attend_warps<2>());
+  s.blocks = s.per_pass > 4 ? 2 : (gqa > 1 ? 1 : 0);
+  s.warps = s.blocks == 0 ? attend_warps<0>() : (s.blocks == 1 ? attend_warps<1>() : attend_warps<2>());
+  const long long warps = static_cast<long long>(kMaxCtas) * s.warps;
   const long long heads_all = rows * heads * s.passes;
   s.workers = heads_all == 0 || max_units > warps / heads_all ? warps : heads_all * max_units;
   return s;
@@ -1106,7 +1512,7 @@ size_t ticket_bytes(long long rows, int heads, const Shape& s) {
 
 size_t attend_workspace_bytes(long long rows, int heads, int gqa, long long max_units) {
   const Shape s = shape_of(rows, heads, gqa, max_units);
-  const size_t part = static_cast<size_t>(s.workers) * 2 * 4 * s.blocks * kPart * sizeof(float);
+  const size_t part = static_cast<size_t>(s.workers) * 2 * (s.blocks == 0 ? 1 : 4 * s.blocks) * kPart * sizeof(float);
   return ticket_bytes(rows, heads, s) + ((part + 255) & ~static_cast<size_t>(255));
 }
 
@@ -1122,13 +1528,12 @@ cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* wor
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int warps = s.blocks == 1 ? attend_warps<1>() : attend_warps<2>();
   long long ctas = sms < kMaxCtas ? sms : kMaxCtas;
   // a worker per warp at most: fewer CTAs than SMs only where fewer units can exist
-  if (ctas * warps > s.workers) ctas = s.workers < ctas ? s.workers : ctas;
-  if (bits == 2)
-    return s.blocks == 1 ? launch<2, 1>(a, static_cast<int>(ctas), stream) : launch<2, 2>(a, static_cast<int>(ctas), stream);
-  return s.blocks == 1 ? launch<4, 1>(a, static_cast<int>(ctas), stream) : launch<4, 2>(a, static_cast<int>(ctas), stream);
+  if (ctas * s.warps > s.workers) ctas = s.workers < ctas ? s.workers : ctas;
+  const int n = static_cast<int>(ctas);
+  if (bits == 2) return s.blocks == 0 ? launch<2, 0>(a, n, stream) : (s.blocks == 1 ? launch<2, 1>(a, n, stream) : launch<2, 2>(a, n, stream));
+  return s.blocks == 0 ? launch<4, 0>(a, n, stream) : (s.blocks == 1 ? launch<4, 1>(a, n, stream) : launch<4, 2>(a, n, stream));
 }
 
 }  // namespace kivi
