@@ -58,11 +58,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
@@ -275,9 +270,21 @@ struct __align__(128) WarpSmem {
   uint4 p[NB == 0 ? 1 : NB][NB == 0 ? 32 : (BITS == 2 ? 128 : 64)];  // P operands
   uint4 qh[NB == 0 ? 1 : NB][NB == 0 ? 1 : 4][32];                   // Q operands (NB > 0: before s, each lane's share)
   uint4 zero4;                        // NB == 0: the operand of the other tile of a pair
+  float part[kQueries * kPart];       // of the warp's first head, where that is not whole (of its last head: in k)
   Cursor cur, now;                    // of the unit fetched last, and of the head in hand
 };
-static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes, "a buffer holds either kind of half");
+static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes && kResTokens * kRow >= 8 * kPart * 4,
+              "a buffer holds either kind of half, and the partials of a warp's last head");
+
+// How `total` units are cut: worker w has those from start(w) on.  Workers of a CTA (`per_cta` of them) are neighbours.
+struct Split {
+  uint32_t total, workers, per_cta, len, longer;  // len units each, one more for the first `longer`
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * len + min(w, longer); }
+  __device__ __forceinline__ uint32_t worker_of(uint32_t f) const {
+    const uint32_t cut = longer * (len + 1);
+    return f < cut ? f / (len + 1) : longer + (f - cut) / len;
+  }
+};
 
 // A warp's walk over its range of units: what is fetched when, where the halves land, and the ends of heads.  Core is the
 // arithmetic: start_head, quant_k, quant_v, Res (state of residual rows) with res_start, res_k, res_v and res_end, finish.
@@ -292,7 +299,6 @@ struct Walker {
   const AttendArgs& a;
   Smem& S;
   const int lane, g, t;
-  long long worker, workers, total;
 
   // the unit fetched last: its index among the row's units of codes or residual rows, how many plain successors it has,
   // whether it can be read, and where it is
@@ -412,96 +418,139 @@ struct Walker {
     return tok < n.len && (tok < n.sink_end || tok >= n.start);
   }
 
-  // Worker whose range holds unit f: ranges start at floor(total w / workers).
-  __device__ static __forceinline__ long long worker_of(long long f, long long workers, long long total) {
-    return ((f + 1) * workers + total - 1) / total - 1;
+  // ---- heads that several warps share ----------------------------------------------------------------------------
+  // Partials (m, l, Z, o[128] of each query) are joined by log-sum-exp: those of a CTA's warps in shared memory by the warp that
+  // arrives last at the head's ticket there, and those of several CTAs in global memory by the one that arrives last at the
+  // head's ticket there.  Parts are taken in their order, so the result does not depend on who arrives when.
+  struct Sums {
+    float m, l, Z, o[4];  // channels 4 lane .. 4 lane + 3
+  };
+  __device__ static __forceinline__ void store_row(uint16_t* out, int lane, const Sums& s) {
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+    *reinterpret_cast<uint2*>(out + 4 * lane) =
+        make_uint2(pack_h2((s.o[0] + s.Z) * inv, (s.o[1] + s.Z) * inv), pack_h2((s.o[2] + s.Z) * inv, (s.o[3] + s.Z) * inv));
   }
-
-  // The workers that hold a part of a head left one partial each: the first of them in its slot 1
-  // unless its range starts with the head, the others in their slot 0.  Lane i reads (m, l, Z) of part i;
-  // the o rows follow with 16 loads in flight.
-  __device__ __noinline__ static void merge(const AttendArgs& a, int s, int e, int units, long long f0, long long workers,
-                                            long long total) {
-    const int lane = threadIdx.x & 31;
-    const long long w0 = worker_of(f0, workers, total), w1 = worker_of(f0 + units - 1, workers, total);
-    const int parts = static_cast<int>(w1 - w0 + 1);
-    const long long first = w0 * 2 + (total * w0 / workers >= f0 ? 0 : 1);
-    const int h = e / a.passes, p0 = (e - h * a.passes) * a.per_pass, nq = min(a.per_pass, a.gqa - p0);
+  __device__ static __forceinline__ uint16_t* out_row(const AttendArgs& a, int seq, int he, int q) {
+    const int h = a.passes == 1 ? he : he / a.passes;
     bool bad = false;
-    uint16_t* out = a.out + (static_cast<size_t>(q_row(a, s, &bad)) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa + p0) * kHeadDim;
-    auto part = [&](int k, int q) { return a.partials + ((k == 0 ? first : (w0 + k) * 2) * NQ + q) * kPart; };
-    constexpr int CH = 16 / NQ;  // parts whose rows are in flight together
-    float mx[NQ], ls[NQ], zs[NQ], acc[NQ][4];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      mx[q] = kNoMax;
-      ls[q] = zs[q] = acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    return a.out + (static_cast<size_t>(q_row(a, seq, &bad)) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa +
+                    (he - h * a.passes) * a.per_pass + q) * kHeadDim;
+  }
+  // This warp's part of a head of `units` units from f0 on is in its shared memory.  warps: the CTA's WarpSmem array.
+  __device__ __noinline__ static void join(const AttendArgs& a, Smem* warps, int* tickets, const Split& sp, uint32_t me, int seq, int he,
+                                           uint32_t f0, uint32_t units) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t w0 = sp.worker_of(f0), w1 = sp.worker_of(f0 + units - 1);
+    const uint32_t cta = me / sp.per_cta, c0 = max(w0, cta * sp.per_cta), c1 = min(w1, (cta + 1) * sp.per_cta - 1);
+    const int first = static_cast<int>(c0 - cta * sp.per_cta), n = static_cast<int>(c1 - c0) + 1;
+    __syncwarp();
+    int last = 1;
+    if (n > 1) {  // one ticket per warp: a warp is the first of one such head at most, its last one
+      if (lane == 0) {
+        __threadfence_block();
+        last = atomicAdd(tickets + first, 1) == n - 1;
+        __threadfence_block();
+      }
+      if (!__shfl_sync(kFull, last, 0)) return;
     }
-    if (parts > 32) {  // the largest reference first; up to 32 parts find it below
-      for (int k = lane; k < parts; k += 32)
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (q < nq) mx[q] = fmaxf(mx[q], __ldcg(part(k, q)));
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) mx[q] = warp_max(mx[q]);
-    }
+    const int h = a.passes == 1 ? he : he / a.passes;
+    const int nq = min(a.per_pass, a.gqa - (he - h * a.passes) * a.per_pass);
+    const bool whole = c0 == w0 && c1 == w1;
+    // only the first of the warps can have started before the head: its part is then in k
+    const float* part0 = sp.start(c0) >= f0 ? warps[first].part : reinterpret_cast<const float*>(warps[first].k);
+    // a CTA's partial heads: the one it starts in (slot 0) and the one it ends in
+    float* mine = a.partials + static_cast<size_t>(2 * cta + (sp.start(cta * sp.per_cta) >= f0 ? 0 : 1)) * NQ * kPart;
 #pragma unroll 1
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      float4 x[NQ];
-      float w[NQ];
+    for (int q = 0; q < nq; ++q) {
+      Sums s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const float* p = (i == 0 ? part0 : warps[first + i].part) + q * kPart;
+        const float4 x = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
+        const float mn = fmaxf(s.m, x.x), f = ex2(s.m - mn), w = ex2(x.x - mn);
+        s.m = mn;
+        s.l = fmaf(s.l, f, w * x.y);
+        s.Z = fmaf(s.Z, f, w * x.z);
+        s.o[0] = fmaf(s.o[0], f, w * v.x);
+        s.o[1] = fmaf(s.o[1], f, w * v.y);
+        s.o[2] = fmaf(s.o[2], f, w * v.z);
+        s.o[3] = fmaf(s.o[3], f, w * v.w);
+      }
+      if (whole) {
+        store_row(out_row(a, seq, he, q), lane, s);
+      } else {
+        if (lane == 0) *reinterpret_cast<float4*>(mine + q * kPart) = make_float4(s.m, s.l, s.Z, 0.f);
+        *reinterpret_cast<float4*>(mine + q * kPart + 4 + 4 * lane) = make_float4(s.o[0], s.o[1], s.o[2], s.o[3]);
+      }
+    }
+    if (whole) return;
+    // one fence publishes the CTA's partial before its ticket
+    __threadfence();
+    __syncwarp();
+    const uint32_t b0 = w0 / sp.per_cta, b1 = w1 / sp.per_cta;
+    const size_t ticket = static_cast<size_t>(seq) * a.heads * a.passes + he;
+    if (lane == 0) {
+      last = atomicAdd(a.tickets + ticket, 1) == static_cast<int>(b1 - b0);
+      if (last) __threadfence();
+    }
+    if (!__shfl_sync(kFull, last, 0)) return;
+    __threadfence();
+    if (lane == 0) a.tickets[ticket] = 0;
+    const size_t begin = 2 * static_cast<size_t>(b0) + (sp.start(b0 * sp.per_cta) >= f0 ? 0 : 1);
+    const int parts = static_cast<int>(b1 - b0) + 1;
+    constexpr int CH = NQ == 1 ? 8 : (NQ == 4 ? 3 : 2);  // parts whose loads are in flight together
+    Sums s[NQ];
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
-        x[q] = q < nq && k0 + lane < parts ? __ldcg(reinterpret_cast<const float4*>(part(k0 + lane, q))) : make_float4(kNoMax, 0.f, 0.f, 0.f);
+    for (int q = 0; q < NQ; ++q) s[q] = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+    for (int i = 0; i < parts; i += CH) {
+      float4 x[CH][NQ], v[CH][NQ];
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          const float* p = a.partials + ((i + j == 0 ? begin : 2 * static_cast<size_t>(b0 + i + j)) * NQ + q) * kPart;
+          const bool in = i + j < parts && q < nq;
+          x[j][q] = in ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(kNoMax, 0.f, 0.f, 0.f);
+          v[j][q] = in ? __ldcg(reinterpret_cast<const float4*>(p + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        if (parts <= 32) mx[q] = warp_max(x[q].x);
-        w[q] = ex2(x[q].x - mx[q]);
-        ls[q] = fmaf(w[q], x[q].y, ls[q]);
-        zs[q] = fmaf(w[q], x[q].z, zs[q]);
-      }
-      const int n = min(32, parts - k0);
-#pragma unroll 1
-      for (int i = 0; i < n; i += CH) {
-        float4 v[CH][NQ];
+        float mn = s[q].m;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
+        for (int j = 0; j < CH; ++j) mn = fmaxf(mn, x[j][q].x);
+        const float f = ex2(s[q].m - mn);
+        s[q].m = mn;
+        s[q].l *= f;
+        s[q].Z *= f;
 #pragma unroll
-          for (int q = 0; q < NQ; ++q)
-            v[j][q] = i + j < n && q < nq ? __ldcg(reinterpret_cast<const float4*>(part(k0 + i + j, q) + 4) + lane)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < 4; ++e) s[q].o[e] *= f;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const float wj = __shfl_sync(kFull, w[q], (i + j) & 31);
-            acc[q][0] = fmaf(wj, v[j][q].x, acc[q][0]);
-            acc[q][1] = fmaf(wj, v[j][q].y, acc[q][1]);
-            acc[q][2] = fmaf(wj, v[j][q].z, acc[q][2]);
-            acc[q][3] = fmaf(wj, v[j][q].w, acc[q][3]);
-          }
+        for (int j = 0; j < CH; ++j) {
+          const float w = ex2(x[j][q].x - mn);
+          s[q].l = fmaf(w, x[j][q].y, s[q].l);
+          s[q].Z = fmaf(w, x[j][q].z, s[q].Z);
+          s[q].o[0] = fmaf(w, v[j][q].x, s[q].o[0]);
+          s[q].o[1] = fmaf(w, v[j][q].y, s[q].o[1]);
+          s[q].o[2] = fmaf(w, v[j][q].z, s[q].o[2]);
+          s[q].o[3] = fmaf(w, v[j][q].w, s[q].o[3]);
+        }
       }
     }
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const float l1 = warp_sum(ls[q]), z1 = warp_sum(zs[q]), inv = l1 == 0.f ? 0.f : 1.f / l1;
-      if (q < nq)
-        *reinterpret_cast<uint2*>(out + q * kHeadDim + 4 * lane) =
-            make_uint2(pack_h2((acc[q][0] + z1) * inv, (acc[q][1] + z1) * inv), pack_h2((acc[q][2] + z1) * inv, (acc[q][3] + z1) * inv));
-    }
-    if (lane == 0) a.tickets[static_cast<size_t>(s) * a.heads * a.passes + e] = 0;
+    for (int q = 0; q < NQ; ++q)
+      if (q < nq) store_row(out_row(a, seq, he, q), lane, s[q]);
   }
 
-  __device__ __forceinline__ void run(long long w, long long nw, long long all, int seq0, long long rem) {
+  // worker: of the split; seq0: row of its first unit, the row's units before it: rem.
+  __device__ __forceinline__ void run(Smem* warps, int* tickets, const Split& split, uint32_t worker, int seq0, uint32_t rem) {
     Core& core = static_cast<Core&>(*this);
-    worker = w;
-    workers = nw;
-    total = all;
-    const long long f0 = total * w / workers;
-    int left = static_cast<int>(total * (w + 1) / workers - f0);  // below 2^31: rows * units a head are
+    const uint32_t f0 = split.start(worker);
+    int left = static_cast<int>(split.start(worker + 1) - f0);
     {
       bool bad;
-      const int n = units_of<UT>(span_of(a, seq0, &bad)).total, he = static_cast<int>(rem / n);
-      take(enter<UT>(a, S.cur, seq0, he, static_cast<int>(rem - static_cast<long long>(he) * n), true));
+      const uint32_t n = units_of<UT>(span_of(a, seq0, &bad)).total, he = rem / n;
+      take(enter<UT>(a, S.cur, seq0, static_cast<int>(he), static_cast<int>(rem - he * n), true));
       steps_ = 0;
       slot = 0;
       head = true;
@@ -511,12 +560,8 @@ struct Walker {
     issue_v(true);
     uint32_t kp = 0, vp = 0;
     load_pairs(kp, vp);
-    struct Head {
-      int seq, he, units;
-      long long f0;
-    } pend[2];
-    int npend = 0;
-    long long at = f0;
+    uint32_t at = f0, first_f0 = 0, first_units = 0;
+    int first_seq = -1, first_he = 0;  // the first head, where it is not whole
     while (left > 0) {
       const Cursor& c = S.cur;
       const int s = c.seq, e = c.he, l0 = c.local, units = c.un.total;
@@ -573,34 +618,21 @@ struct Walker {
         core.res_end(r);
       }
       const bool whole = count == units;
-      core.finish(whole, at == f0 ? 0 : 1);
-      if (!whole) {
-        pend[npend].seq = s;
-        pend[npend].he = e;
-        pend[npend].units = units;
-        pend[npend].f0 = at - l0;
-        ++npend;
+      if (whole) {
+        core.finish(nullptr);
+      } else if (at == f0) {
+        core.finish(S.part);
+        first_seq = s;
+        first_he = e;
+        first_f0 = at - l0;
+        first_units = units;
+      } else {  // the last head: no copy is in flight any more
+        core.finish(reinterpret_cast<float*>(S.k));
+        join(a, warps, tickets, split, worker, s, e, at - l0, units);
       }
       at += count;
     }
-    if (npend == 0) return;
-    // one fence publishes this warp's partials before its tickets; the last part of a head joins it
-    __threadfence();
-    __syncwarp();
-    int last = 0;
-    if (lane == 0) {
-      for (int i = 0; i < npend; ++i) {
-        const int others = static_cast<int>(worker_of(pend[i].f0 + pend[i].units - 1, workers, total) - worker_of(pend[i].f0, workers, total));
-        if (atomicAdd(a.tickets + static_cast<size_t>(pend[i].seq) * a.heads * a.passes + pend[i].he, 1) == others) last |= 1 << i;
-      }
-      if (last) __threadfence();
-    }
-    last = __shfl_sync(kFull, last, 0);
-    if (!last) return;
-    __threadfence();
-#pragma unroll 1
-    for (int i = 0; i < npend; ++i)
-      if ((last >> i) & 1) merge(a, pend[i].seq, pend[i].he, pend[i].units, pend[i].f0, workers, total);
+    if (first_seq >= 0) join(a, warps, tickets, split, worker, first_seq, first_he, first_f0, first_units);
   }
 };
 
@@ -608,7 +640,7 @@ struct Walker {
 template <int BITS, int NB>
 struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   using Base = Walker<BITS, NB, Many<BITS, NB>>;
-  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full, Base::worker;
+  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full;
   using Base::UT, Base::PT, Base::P, Base::NQ, Base::seen;
   static constexpr int HP = P / 2;                  // code pairs per word
   static constexpr int MT = UT / 16;                // K tiles per unit
@@ -1046,7 +1078,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
 
   // ---- the end of a head's segment -----------------------------------------------------------------------
   // Lane (g, t): o of query t (each column block), channels 16 g .. 16 g + 15.
-  __device__ void finish(bool whole, int slot) {
+  __device__ __forceinline__ void finish(float* part) {
     const int nq = S.now.queries;
     const float back = pow2i(eref);
 #pragma unroll
@@ -1065,7 +1097,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         f[2 * v8] = (o[b][v8][0] + o[b][v8][1]) * back;
         f[2 * v8 + 1] = (o[b][v8][2] + o[b][v8][3]) * back;
       }
-      if (whole) {
+      if (part == nullptr) {
         const float inv = ls == 0.f ? 0.f : 1.f / ls;
         uint32_t w[8];
 #pragma unroll
@@ -1075,7 +1107,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
-        float* dst = a.partials + ((worker * 2 + slot) * NQ + qi) * kPart;
+        float* dst = part + qi * kPart;
         if (g == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m[b], ls, zs, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1115,7 +1147,7 @@ __device__ __forceinline__ float reciprocal(float x) {
 template <int BITS>
 struct One : Walker<BITS, 0, One<BITS>> {
   using Base = Walker<BITS, 0, One<BITS>>;
-  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full, Base::worker;
+  using Base::a, Base::S, Base::lane, Base::g, Base::t, Base::slot_now, Base::full_from, Base::sink_full;
   using Base::UT, Base::PT, Base::P, Base::seen;
   static constexpr int NV = P / 4;            // copies of a word: 4 at 2 bits, 2 at 4 bits
   static constexpr int W = 1 << (BITS * (NV - 1));
@@ -1403,16 +1435,13 @@ struct One : Walker<BITS, 0, One<BITS>> {
     __syncwarp();
   }
 
-  __device__ __forceinline__ void finish(bool whole, int slot) {
-    const float ls = warp_sum(l), zs = warp_sum(Z);
-    if (whole) {
-      const float inv = ls == 0.f ? 0.f : 1.f / ls;
-      *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(S.now.row) * a.heads * a.gqa + S.now.q0) * kHeadDim + 4 * lane) =
-          make_uint2(pack_h2((o[0] + zs) * inv, (o[1] + zs) * inv), pack_h2((o[2] + zs) * inv, (o[3] + zs) * inv));
+  __device__ __forceinline__ void finish(float* part) {
+    const typename Base::Sums s = {m, warp_sum(l), warp_sum(Z), {o[0], o[1], o[2], o[3]}};
+    if (part == nullptr) {
+      Base::store_row(a.out + (static_cast<size_t>(S.now.row) * a.heads * a.gqa + S.now.q0) * kHeadDim, lane, s);
     } else {
-      float* dst = a.partials + (worker * 2 + slot) * kPart;
-      if (lane == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m, ls, zs, 0.f);
-      *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(s.l == 0.f ? kNoMax : m, s.l, s.Z, 0.f);
+      *reinterpret_cast<float4*>(part + 4 + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
     }
   }
 };
@@ -1431,7 +1460,7 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   constexpr int W = attend_warps<NB>(), T = W * 32, UT = CoreOf<BITS, NB>::type::UT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = WarpSmem<BITS, NB>;
-  __shared__ int warp_sum[W], cum[T + 1];  // units per head before each thread's rows
+  __shared__ int warp_sum[W], tickets[W], cum[T + 1];  // units per head before each thread's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.rows + T - 1) / T, r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
   int mine = 0;
@@ -1448,20 +1477,26 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_sum[warp] = x;
+  if (lane == 0) tickets[warp] = 0;
   __syncthreads();
   int before = x - mine;
   for (int i = 0; i < warp; ++i) before += warp_sum[i];
   cum[tid] = before;
   if (tid == T - 1) cum[T] = before + mine;
   __syncthreads();
-  const long long he_count = static_cast<long long>(a.heads) * a.passes;
-  const long long total = cum[T] * he_count;
-  const long long workers = min(total, static_cast<long long>(gridDim.x) * W);
-  // neighbouring workers on different SMs: few units spread over the GPU
-  const long long worker = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-  if (worker >= workers) return;
+  const uint32_t he_count = static_cast<uint32_t>(a.heads) * a.passes;
+  Split split;
+  split.total = static_cast<uint32_t>(cum[T]) * he_count;  // below 2^32: checked on the host
+  if (split.total == 0) return;
+  // few units spread over the SMs
+  split.per_cta = min(static_cast<uint32_t>(W), (split.total + gridDim.x - 1) / gridDim.x);
+  split.workers = min(split.total, gridDim.x * split.per_cta);
+  split.len = split.total / split.workers;
+  split.longer = split.total - split.len * split.workers;
+  const uint32_t worker = blockIdx.x * split.per_cta + warp;
+  if (warp >= split.per_cta || worker >= split.workers) return;
   // the row of the worker's first unit: its thread's rows by bisection, then one by one
-  const long long f0 = total * worker / workers;
+  const uint32_t f0 = split.start(worker);
   const int want = static_cast<int>(f0 / he_count);
   int lo = 0, hi = T;  // cum[lo] <= want < cum[hi]
   while (hi - lo > 1) {
@@ -1473,14 +1508,15 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   }
   int row = lo * per, first = cum[lo];
   for (int n; first + (n = row_units<UT>(a, row)) <= want; ++row) first += n;
-  typename CoreOf<BITS, NB>::type d(a, reinterpret_cast<Smem*>(smem_raw)[warp], lane);
-  d.run(worker, workers, total, row, f0 - first * he_count);
+  Smem* warps = reinterpret_cast<Smem*>(smem_raw);
+  typename CoreOf<BITS, NB>::type d(a, warps[warp], lane);
+  d.run(warps, tickets, split, worker, row, f0 - first * he_count);
 }
 
 template <int BITS, int NB>
 cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
   constexpr int smem = attend_warps<NB>() * static_cast<int>(sizeof(WarpSmem<BITS, NB>));
-  static_assert(smem + 4 * (attend_warps<NB>() * 33 + 1) <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
+  static_assert(smem + 4 * (attend_warps<NB>() * 34 + 1) <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(attend_kernel<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -1490,18 +1526,12 @@ cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
 
 struct Shape {
   int passes, per_pass, blocks;  // query passes per KV head, queries of a pass, column blocks of four (0: one query)
-  int warps;                     // per CTA
-  long long workers;             // at most
 };
-Shape shape_of(long long rows, int heads, int gqa, long long max_units) {
+Shape shape_of(int gqa) {
   Shape s;
   s.passes = (gqa + 7) / 8;
   s.per_pass = (gqa + s.passes - 1) / s.passes;
   s.blocks = s.per_pass > 4 ? 2 : (gqa > 1 ? 1 : 0);
-  s.warps = s.blocks == 0 ? attend_warps<0>() : (s.blocks == 1 ? attend_warps<1>() : attend_warps<2>());
-  const long long warps = static_cast<long long>(kMaxCtas) * s.warps;
-  const long long heads_all = rows * heads * s.passes;
-  s.workers = heads_all == 0 || max_units > warps / heads_all ? warps : heads_all * max_units;
   return s;
 }
 size_t ticket_bytes(long long rows, int heads, const Shape& s) {
@@ -1511,14 +1541,15 @@ size_t ticket_bytes(long long rows, int heads, const Shape& s) {
 }  // namespace
 
 size_t attend_workspace_bytes(long long rows, int heads, int gqa, long long max_units) {
-  const Shape s = shape_of(rows, heads, gqa, max_units);
-  const size_t part = static_cast<size_t>(s.workers) * 2 * (s.blocks == 0 ? 1 : 4 * s.blocks) * kPart * sizeof(float);
+  const Shape s = shape_of(gqa);
+  if (rows * max_units > 0xffffffffll / (static_cast<long long>(heads) * s.passes)) return 0;
+  const size_t part = static_cast<size_t>(kMaxCtas) * 2 * (s.blocks == 0 ? 1 : 4 * s.blocks) * kPart * sizeof(float);
   return ticket_bytes(rows, heads, s) + ((part + 255) & ~static_cast<size_t>(255));
 }
 
-cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* workspace, cudaStream_t stream) {
+cudaError_t launch_attend(AttendArgs a, int bits, void* workspace, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const Shape s = shape_of(a.max_rows, a.heads, a.gqa, max_units);
+  const Shape s = shape_of(a.gqa);
   a.passes = s.passes;
   a.per_pass = s.per_pass;
   a.lg_upb = a.lg_r - (bits == 2 ? 7 : 6);
@@ -1528,10 +1559,7 @@ cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* wor
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  long long ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  // a worker per warp at most: fewer CTAs than SMs only where fewer units can exist
-  if (ctas * s.warps > s.workers) ctas = s.workers < ctas ? s.workers : ctas;
-  const int n = static_cast<int>(ctas);
+  const int n = sms < kMaxCtas ? sms : kMaxCtas;
   if (bits == 2) return s.blocks == 0 ? launch<2, 0>(a, n, stream) : (s.blocks == 1 ? launch<2, 1>(a, n, stream) : launch<2, 2>(a, n, stream));
   return s.blocks == 0 ? launch<4, 0>(a, n, stream) : (s.blocks == 1 ? launch<4, 1>(a, n, stream) : launch<4, 2>(a, n, stream));
 }

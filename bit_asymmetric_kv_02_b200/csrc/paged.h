@@ -81,8 +81,8 @@ struct AttendArgs {
 };
 constexpr int kAttendResTokens = 16;  // tokens of a residual unit
 constexpr int attend_unit_tokens(int bits) { return 256 / bits; }
-// max_units: units (of codes and of residual rows) a head can have; rows * max_units below 2^31.
+// max_units: units (of codes and of residual rows) a head can have.  0: more units in all than 32 bits count.
 size_t attend_workspace_bytes(long long rows, int heads, int gqa, long long max_units);
-cudaError_t launch_attend(AttendArgs a, int bits, long long max_units, void* workspace, cudaStream_t stream);
+cudaError_t launch_attend(AttendArgs a, int bits, void* workspace, cudaStream_t stream);
 
 }  // namespace kivi

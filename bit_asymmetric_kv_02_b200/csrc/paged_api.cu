@@ -71,7 +71,7 @@ long long max_units(int bits, int residual, long long blocks) {
   return blocks * (residual / kivi::attend_unit_tokens(bits)) + residual / kivi::kAttendResTokens;
 }
 
-// Workspace of max_rows rows; 0 where the rows' units are past the kernel's 32-bit prefix sums.
+// Workspace of max_rows rows; 0 where the units are past the kernel's 32-bit counts.
 size_t attend_bytes(int max_rows, int heads, int num_q_heads, long long units) {
   if (num_q_heads < 1 || num_q_heads % heads != 0 || num_q_heads / heads > kMaxGqa || max_rows > kMaxSeqs) return 0;
   if (max_rows * units > 0x7fffffffll) return 0;
@@ -82,7 +82,7 @@ int run_attend(const kivi::AttendArgs& a, int bits, long long units, void* ws, s
   const size_t need = attend_bytes(a.max_rows, a.heads, a.heads * a.gqa, units);
   if (need == 0) return KIVI_ERR_UNSUPPORTED;
   if (!aligned(ws, 256) || ws_bytes < need) return KIVI_ERR_WORKSPACE;
-  return kivi::launch_attend(a, bits, units, ws, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
+  return kivi::launch_attend(a, bits, ws, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KIVI_OK : KIVI_ERR_CUDA;
 }
 
 bool heads_ok(const kivi_heads* h) {
