@@ -37,7 +37,7 @@ constexpr int kHalfBytes = 4096;                  // the K or the V part of a un
 constexpr int kRow = 272;                         // a residual row in shared memory (ldmatrix without conflicts)
 constexpr int kVPieceStride = 1040;               // V word rows 2 t and 2 t + 1, four bank groups for t = 0..3
 constexpr int kQRow = 272;                        // a raw query row in shared memory
-constexpr int kPart = 132;                        // floats of a partial: m, l, Z, pad, o[128]
+constexpr int kPart = 132;                        // floats of a partial: m, pad, l, Z, o[128]
 constexpr int kMaxCtas = 160;
 constexpr float kNoMax = -1e38f;                  // reference of a part without tokens: finite, and below every other
 constexpr float kSlack = 4.f;                     // logits may pass the reference by this much: weights up to 2^4
@@ -57,6 +57,17 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max_of_warp(float v) {  // one instruction; NaN is ignored
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// Adds 1, ordered behind the warp's earlier writes and before its later reads (with a __syncwarp on either side).
+__device__ __forceinline__ int add_acq_rel(int32_t* p) {
+  int r;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(r) : "l"(p) : "memory");
+  return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -199,6 +210,7 @@ __device__ __forceinline__ int row_units(const AttendArgs& a, int i) {
 // Where a warp is: unit `local` of a head (KV head and query pass he) of row seq.
 struct Cursor {
   int seq, he, local;
+  uint32_t f0;                  // of the split: the head's first unit (set for a head in hand)
   int row, q0, queries;  // row of q and out, first query head and queries of the pass
   Units un;
   Span sp;
@@ -271,18 +283,26 @@ struct __align__(128) WarpSmem {
   uint4 qh[NB == 0 ? 1 : NB][NB == 0 ? 1 : 4][32];                   // Q operands (NB > 0: before s, each lane's share)
   uint4 zero4;                        // NB == 0: the operand of the other tile of a pair
   float part[kQueries * kPart];       // of the warp's first head, where that is not whole (of its last head: in k)
-  Cursor cur, now;                    // of the unit fetched last, and of the head in hand
+  Cursor cur, now, first;             // of the unit fetched last, of the head in hand, and of the warp's first head
 };
 static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes && kResTokens * kRow >= 8 * kPart * 4,
               "a buffer holds either kind of half, and the partials of a warp's last head");
 
+// x / d with recip = floor((2^32 - 1) / d): the product's upper word is at most two short.
+__device__ __forceinline__ uint32_t divide(uint32_t x, uint32_t d, uint32_t recip) {
+  uint32_t q = __umulhi(x, recip), r = x - q * d;
+  if (r >= d) r -= d, ++q;
+  if (r >= d) ++q;
+  return q;
+}
 // How `total` units are cut: worker w has those from start(w) on.  Workers of a CTA (`per_cta` of them) are neighbours.
 struct Split {
   uint32_t total, workers, per_cta, len, longer;  // len units each, one more for the first `longer`
+  uint32_t recip, recip1, recip_cta;              // of len, len + 1 and per_cta
   __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * len + min(w, longer); }
   __device__ __forceinline__ uint32_t worker_of(uint32_t f) const {
-    const uint32_t cut = longer * (len + 1);
-    return f < cut ? f / (len + 1) : longer + (f - cut) / len;
+    const uint32_t cut = longer * (len + 1), more = f < cut ? 1 : 0;
+    return (more ? 0 : longer) + divide(more ? f : f - cut, len + more, more ? recip1 : recip);
   }
 };
 
@@ -419,7 +439,7 @@ struct Walker {
   }
 
   // ---- heads that several warps share ----------------------------------------------------------------------------
-  // Partials (m, l, Z, o[128] of each query) are joined by log-sum-exp: those of a CTA's warps in shared memory by the warp that
+  // Partials (m, l, Z and o[128] of each query) are joined by log-sum-exp: those of a CTA's warps in shared memory by the warp that
   // arrives last at the head's ticket there, and those of several CTAs in global memory by the one that arrives last at the
   // head's ticket there.  Parts are taken in their order, so the result does not depend on who arrives when.
   struct Sums {
@@ -430,116 +450,123 @@ struct Walker {
     *reinterpret_cast<uint2*>(out + 4 * lane) =
         make_uint2(pack_h2((s.o[0] + s.Z) * inv, (s.o[1] + s.Z) * inv), pack_h2((s.o[2] + s.Z) * inv, (s.o[3] + s.Z) * inv));
   }
-  __device__ static __forceinline__ uint16_t* out_row(const AttendArgs& a, int seq, int he, int q) {
-    const int h = a.passes == 1 ? he : he / a.passes;
-    bool bad = false;
-    return a.out + (static_cast<size_t>(q_row(a, seq, &bad)) * a.heads * a.gqa + static_cast<size_t>(h) * a.gqa +
-                    (he - h * a.passes) * a.per_pass + q) * kHeadDim;
-  }
-  // This warp's part of a head of `units` units from f0 on is in its shared memory.  warps: the CTA's WarpSmem array.
-  __device__ __noinline__ static void join(const AttendArgs& a, Smem* warps, int* tickets, const Split& sp, uint32_t me, int seq, int he,
-                                           uint32_t f0, uint32_t units) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t w0 = sp.worker_of(f0), w1 = sp.worker_of(f0 + units - 1);
-    const uint32_t cta = me / sp.per_cta, c0 = max(w0, cta * sp.per_cta), c1 = min(w1, (cta + 1) * sp.per_cta - 1);
-    const int first = static_cast<int>(c0 - cta * sp.per_cta), n = static_cast<int>(c1 - c0) + 1;
-    __syncwarp();
-    int last = 1;
-    if (n > 1) {  // one ticket per warp: a warp is the first of one such head at most, its last one
-      if (lane == 0) {
-        __threadfence_block();
-        last = atomicAdd(tickets + first, 1) == n - 1;
-        __threadfence_block();
-      }
-      if (!__shfl_sync(kFull, last, 0)) return;
+  // s joined with the n <= 32 parts at p0, p + stride, p + 2 stride, ..: lane i weighs part i, so that the rows follow without
+  // a chain of maxima.
+  __device__ static __forceinline__ void add_parts(Sums& s, int lane, const float* p0, const float* p, int stride, int n) {
+    float mi = kNoMax;
+    if (lane < n) mi = lane == 0 ? *p0 : p[lane * stride];
+    const float mn = fmaxf(s.m, max_of_warp(mi)), f = ex2(s.m - mn), w = ex2(mi - mn);
+    s.m = mn;
+    s.l *= f;
+    s.Z *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.o[e] *= f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* at = i == 0 ? p0 : p + i * stride;
+      const float2 x = *reinterpret_cast<const float2*>(at + 2);  // l, Z
+      const float4 v = *reinterpret_cast<const float4*>(at + 4 + 4 * lane);
+      const float wi = __shfl_sync(kFull, w, i);
+      s.l = fmaf(wi, x.x, s.l);
+      s.Z = fmaf(wi, x.y, s.Z);
+      s.o[0] = fmaf(wi, v.x, s.o[0]);
+      s.o[1] = fmaf(wi, v.y, s.o[1]);
+      s.o[2] = fmaf(wi, v.z, s.o[2]);
+      s.o[3] = fmaf(wi, v.w, s.o[3]);
     }
-    const int h = a.passes == 1 ? he : he / a.passes;
-    const int nq = min(a.per_pass, a.gqa - (he - h * a.passes) * a.per_pass);
-    const bool whole = c0 == w0 && c1 == w1;
+  }
+  // The warps of this CTA that hold parts of head c: first .. first + n - 1; w0 and w1 are its first and last worker.
+  struct Sharers {
+    uint32_t w0, w1;
+    int first, n;
+  };
+  __device__ static __forceinline__ Sharers sharers(const Split& sp, const Cursor& c) {
+    const uint32_t w0 = sp.worker_of(c.f0), w1 = sp.worker_of(c.f0 + c.un.total - 1), lo = blockIdx.x * sp.per_cta;
+    const uint32_t c0 = max(w0, lo), c1 = min(w1, lo + sp.per_cta - 1);
+    return {w0, w1, static_cast<int>(c0 - lo), static_cast<int>(c1 - c0) + 1};
+  }
+  // This warp's part of head c is in its shared memory: true for the last of the CTA's warps to say so, which joins them.
+  __device__ __noinline__ static bool arrive(int* tickets, const Split& sp, const Cursor& c) {
+    const Sharers h = sharers(sp, c);
+    __syncwarp();
+    if (h.n == 1) return true;
+    int last = 0;
+    if ((threadIdx.x & 31) == 0) {  // one ticket per warp: a warp is the first of one such head at most, its last one
+      __threadfence_block();
+      last = atomicAdd(tickets + h.first, 1) == h.n - 1;
+      __threadfence_block();
+    }
+    return __shfl_sync(kFull, last, 0) != 0;
+  }
+  // Run once or twice per warp, mostly from a cold instruction cache: the loops are kept small, and what comes from global
+  // memory comes in one go through shared memory.  warps: the CTA's WarpSmem array.
+  __device__ __noinline__ static void join(const AttendArgs& a, Smem* warps, const Split& sp, const Cursor& c) {
+    const int lane = threadIdx.x & 31;
+    const Sharers h = sharers(sp, c);
+    const uint32_t cta = blockIdx.x, f0 = c.f0, w0 = h.w0, w1 = h.w1, c0 = cta * sp.per_cta + h.first;
+    const int first = h.first, n = h.n;
+    __syncwarp();
+    const int nq = c.queries;
+    uint16_t* out = a.out + (static_cast<size_t>(c.row) * a.heads * a.gqa + c.q0) * kHeadDim;
+    const bool whole = c0 == w0 && c0 + n - 1 == w1;
     // only the first of the warps can have started before the head: its part is then in k
     const float* part0 = sp.start(c0) >= f0 ? warps[first].part : reinterpret_cast<const float*>(warps[first].k);
     // a CTA's partial heads: the one it starts in (slot 0) and the one it ends in
     float* mine = a.partials + static_cast<size_t>(2 * cta + (sp.start(cta * sp.per_cta) >= f0 ? 0 : 1)) * NQ * kPart;
-#pragma unroll 1
+#pragma unroll 2
     for (int q = 0; q < nq; ++q) {
       Sums s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        const float* p = (i == 0 ? part0 : warps[first + i].part) + q * kPart;
-        const float4 x = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
-        const float mn = fmaxf(s.m, x.x), f = ex2(s.m - mn), w = ex2(x.x - mn);
-        s.m = mn;
-        s.l = fmaf(s.l, f, w * x.y);
-        s.Z = fmaf(s.Z, f, w * x.z);
-        s.o[0] = fmaf(s.o[0], f, w * v.x);
-        s.o[1] = fmaf(s.o[1], f, w * v.y);
-        s.o[2] = fmaf(s.o[2], f, w * v.z);
-        s.o[3] = fmaf(s.o[3], f, w * v.w);
-      }
+      add_parts(s, lane, part0 + q * kPart, warps[first].part + q * kPart, sizeof(Smem) / sizeof(float), n);
       if (whole) {
-        store_row(out_row(a, seq, he, q), lane, s);
+        store_row(out + q * kHeadDim, lane, s);
       } else {
-        if (lane == 0) *reinterpret_cast<float4*>(mine + q * kPart) = make_float4(s.m, s.l, s.Z, 0.f);
+        if (lane == 0) *reinterpret_cast<float4*>(mine + q * kPart) = make_float4(s.m, 0.f, s.l, s.Z);
         *reinterpret_cast<float4*>(mine + q * kPart + 4 + 4 * lane) = make_float4(s.o[0], s.o[1], s.o[2], s.o[3]);
       }
     }
     if (whole) return;
-    // one fence publishes the CTA's partial before its ticket
-    __threadfence();
-    __syncwarp();
-    const uint32_t b0 = w0 / sp.per_cta, b1 = w1 / sp.per_cta;
-    const size_t ticket = static_cast<size_t>(seq) * a.heads * a.passes + he;
-    if (lane == 0) {
-      last = atomicAdd(a.tickets + ticket, 1) == static_cast<int>(b1 - b0);
-      if (last) __threadfence();
-    }
+    __syncwarp();  // every lane's share of the partial comes before the ticket
+    const uint32_t b0 = divide(w0, sp.per_cta, sp.recip_cta), b1 = divide(w1, sp.per_cta, sp.recip_cta);
+    const size_t ticket = static_cast<size_t>(c.seq) * a.heads * a.passes + c.he;
+    int last = 0;
+    if (lane == 0) last = add_acq_rel(a.tickets + ticket) == static_cast<int>(b1 - b0);
     if (!__shfl_sync(kFull, last, 0)) return;
-    __threadfence();
+    __syncwarp();
     if (lane == 0) a.tickets[ticket] = 0;
-    const size_t begin = 2 * static_cast<size_t>(b0) + (sp.start(b0 * sp.per_cta) >= f0 ? 0 : 1);
     const int parts = static_cast<int>(b1 - b0) + 1;
-    constexpr int CH = NQ == 1 ? 8 : (NQ == 4 ? 3 : 2);  // parts whose loads are in flight together
-    Sums s[NQ];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) s[q] = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    const float* part_0 = a.partials + (2 * static_cast<size_t>(b0) + (sp.start(b0 * sp.per_cta) >= f0 ? 0 : 1)) * NQ * kPart;
+    const float* part_i = a.partials + 2 * static_cast<size_t>(b0) * NQ * kPart;
+    // rows of partials that fit behind k (v, q, p and qh are free by now): all queries' at once, or one query's as many as fit
+    Smem& S = warps[threadIdx.x >> 5];
+    float* rows = reinterpret_cast<float*>(S.v);
+    constexpr int kRows = (sizeof(S.v) + sizeof(S.q) + sizeof(S.p) + sizeof(S.qh)) / (kPart * sizeof(float));
+    const int nb = parts * nq <= kRows ? nq : 1, np = nb == 1 ? kRows : parts;
 #pragma unroll 1
-    for (int i = 0; i < parts; i += CH) {
-      float4 x[CH][NQ], v[CH][NQ];
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const float* p = a.partials + ((i + j == 0 ? begin : 2 * static_cast<size_t>(b0 + i + j)) * NQ + q) * kPart;
-          const bool in = i + j < parts && q < nq;
-          x[j][q] = in ? __ldcg(reinterpret_cast<const float4*>(p)) : make_float4(kNoMax, 0.f, 0.f, 0.f);
-          v[j][q] = in ? __ldcg(reinterpret_cast<const float4*>(p + 4) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < nq; q0 += nb) {
+      Sums s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+      for (int i0 = 0; i0 < parts; i0 += np) {
+        const int n2 = min(np, parts - i0);
+        __syncwarp();
+        uint32_t dst = smem_u32(rows) + 16 * lane;
+#pragma unroll 1
+        for (int i = i0; i < i0 + n2; ++i) {  // the rows of a part follow one another, in memory as here
+          const char* src = reinterpret_cast<const char*>((i == 0 ? part_0 : part_i + 2 * static_cast<size_t>(i) * NQ * kPart) + q0 * kPart);
+          const int bytes = nb * kPart * 4;
+#pragma unroll 2
+          for (int at = 16 * lane; at < bytes; at += 512) copy16(dst + at - 16 * lane, src + at);
+          dst += bytes;
         }
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        float mn = s[q].m;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) mn = fmaxf(mn, x[j][q].x);
-        const float f = ex2(s[q].m - mn);
-        s[q].m = mn;
-        s[q].l *= f;
-        s[q].Z *= f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[q].o[e] *= f;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const float w = ex2(x[j][q].x - mn);
-          s[q].l = fmaf(w, x[j][q].y, s[q].l);
-          s[q].Z = fmaf(w, x[j][q].z, s[q].Z);
-          s[q].o[0] = fmaf(w, v[j][q].x, s[q].o[0]);
-          s[q].o[1] = fmaf(w, v[j][q].y, s[q].o[1]);
-          s[q].o[2] = fmaf(w, v[j][q].z, s[q].o[2]);
-          s[q].o[3] = fmaf(w, v[j][q].w, s[q].o[3]);
+        copies_commit();
+        copies_wait<0>();
+#pragma unroll 1
+        for (int q = 0; q < nb; ++q) {
+          if (nb > 1) s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
+          add_parts(s, lane, rows + q * kPart, rows + q * kPart, nb * kPart, n2);
+          if (i0 + n2 == parts) store_row(out + (q0 + q) * kHeadDim, lane, s);
         }
       }
     }
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      if (q < nq) store_row(out_row(a, seq, he, q), lane, s[q]);
   }
 
   // worker: of the split; seq0: row of its first unit, the row's units before it: rem.
@@ -560,14 +587,18 @@ struct Walker {
     issue_v(true);
     uint32_t kp = 0, vp = 0;
     load_pairs(kp, vp);
-    uint32_t at = f0, first_f0 = 0, first_units = 0;
-    int first_seq = -1, first_he = 0;  // the first head, where it is not whole
+    uint32_t at = f0;
+    bool begun = false;  // the first head is this warp's to join, at the end: its buffers are in use until then
     while (left > 0) {
       const Cursor& c = S.cur;
-      const int s = c.seq, e = c.he, l0 = c.local, units = c.un.total;
+      const int l0 = c.local, units = c.un.total;
       const int count = min(left, units - l0), nq = min(count, max(0, c.un.q_units - l0));
       __syncwarp();
-      if (lane == 0) S.now = c;
+      if (lane == 0) {
+        S.now = c;
+        S.now.f0 = at - l0;
+        if (at == f0) S.first = S.now;
+      }
       __syncwarp();
       slot_now = slot;
       full_from = (S.now.sp.start + UT - 1) / UT;
@@ -622,17 +653,14 @@ struct Walker {
         core.finish(nullptr);
       } else if (at == f0) {
         core.finish(S.part);
-        first_seq = s;
-        first_he = e;
-        first_f0 = at - l0;
-        first_units = units;
+        begun = arrive(tickets, split, S.now);
       } else {  // the last head: no copy is in flight any more
         core.finish(reinterpret_cast<float*>(S.k));
-        join(a, warps, tickets, split, worker, s, e, at - l0, units);
+        if (arrive(tickets, split, S.now)) join(a, warps, split, S.now);
       }
       at += count;
     }
-    if (first_seq >= 0) join(a, warps, tickets, split, worker, first_seq, first_he, first_f0, first_units);
+    if (begun) join(a, warps, split, S.first);
   }
 };
 
@@ -1108,7 +1136,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
         float* dst = part + qi * kPart;
-        if (g == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m[b], ls, zs, 0.f);
+        if (g == 0) *reinterpret_cast<float4*>(dst) = make_float4(ls == 0.f ? kNoMax : m[b], 0.f, ls, zs);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(dst + 4 + 16 * g + 4 * i) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
@@ -1132,11 +1160,6 @@ __device__ __forceinline__ void mma_bytes(int (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float max_of_warp(float v) {  // one instruction; NaN is ignored
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
@@ -1440,7 +1463,7 @@ struct One : Walker<BITS, 0, One<BITS>> {
     if (part == nullptr) {
       Base::store_row(a.out + (static_cast<size_t>(S.now.row) * a.heads * a.gqa + S.now.q0) * kHeadDim, lane, s);
     } else {
-      if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(s.l == 0.f ? kNoMax : m, s.l, s.Z, 0.f);
+      if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(s.l == 0.f ? kNoMax : m, 0.f, s.l, s.Z);
       *reinterpret_cast<float4*>(part + 4 + 4 * lane) = make_float4(o[0], o[1], o[2], o[3]);
     }
   }
@@ -1493,6 +1516,9 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   split.workers = min(split.total, gridDim.x * split.per_cta);
   split.len = split.total / split.workers;
   split.longer = split.total - split.len * split.workers;
+  split.recip = 0xffffffffu / split.len;
+  split.recip1 = 0xffffffffu / (split.len + 1);
+  split.recip_cta = 0xffffffffu / split.per_cta;
   const uint32_t worker = blockIdx.x * split.per_cta + warp;
   if (warp >= split.per_cta || worker >= split.workers) return;
   // the row of the worker's first unit: its thread's rows by bisection, then one by one
