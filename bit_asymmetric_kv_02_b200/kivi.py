@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # KIVI_LIB=debug selects the debug build (libkivi_debug.so: device-side bounds checks); any other
@@ -58,6 +59,9 @@ class kivi_heads(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("x_batch", "x_token", "x_head", "y_batch", "y_token", "y_head")]
 
 
+_HEADS = struct.Struct("@PPPii6q")  # kivi_heads
+
+
 class kivi_paged_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("num_pages", "num_seqs", "max_blocks", "num_kv_heads", "head_dim", "bits", "group_k", "group_v",
@@ -94,7 +98,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     I64, F32, F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
     cfgp, cachep = ctypes.POINTER(kivi_config), ctypes.POINTER(kivi_cache)
     pcfgp, pcachep, planp = (ctypes.POINTER(s) for s in (kivi_paged_config, kivi_paged_cache, kivi_paged_plan))
-    rotp, headsp = ctypes.POINTER(kivi_rotary), ctypes.POINTER(kivi_heads)
+    rotp = ctypes.POINTER(kivi_rotary)
     sig = {
         "kivi_abi_version": (I32, []),
         "kivi_strerror": (ctypes.c_char_p, [I32]),
@@ -112,7 +116,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kivi_window_workspace_bytes": (SZ, [cfgp, I32]),
         "kivi_decode_attention_window": (I32, [cfgp, cachep, P, I32, F32, I32, I32, P, P, SZ, P, P]),
         "kivi_rotary_init": (I32, [rotp, I32, I32, F64, I32, F64, F64, F64, I32]),
-        "kivi_rotary_apply": (I32, [rotp, I32, I32, I32, P, I32, headsp, headsp, headsp, F32, P]),
+        "kivi_rotary_apply": (I32, [rotp, I32, I32, I32, P, I32, P, P, P, F32, P]),  # heads: kivi_heads or their bytes
         "kivi_paged_check_config": (I32, [pcfgp]),
         "kivi_paged_sizes": (I32, [pcfgp, ctypes.POINTER(SZ)]),
         "kivi_paged_build_tables": (I32, [pcfgp, pcachep, I32, P, P, P, P, planp, P, P]),
@@ -231,8 +235,8 @@ def kivi_rotary_init(rotary_dim: int, interleaved: int, theta: float, scaling: i
 
 def kivi_rotary_apply(rotary, dtype: int, batch: int, tokens: int, positions_ptr: int | None, position0: int, q, k, v,
                       eps: float, stream: int) -> None:
-    """q, k, v: kivi_heads or None."""
-    ref = [None if h is None else ctypes.byref(h) for h in (q, k, v)]
+    """q, k, v: kivi_heads, the bytes of one, or None."""
+    ref = [ctypes.byref(h) if isinstance(h, kivi_heads) else h for h in (q, k, v)]
     _check(load_library().kivi_rotary_apply(ctypes.byref(rotary), dtype, batch, tokens, positions_ptr, position0, *ref,
                                             eps, stream), "kivi_rotary_apply")
 
@@ -321,6 +325,7 @@ class KiviCache:
         self.ws_ptr = self.workspace.data_ptr() + off
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self._window_ws = {}
+        self.index = self.status.device.index
 
     # views of the buffers in the layout of include/kivi.h
     def view(self, name: str):
@@ -409,19 +414,18 @@ class KiviCache:
         and cleared on its first call, on the current stream: make that call before a capture."""
         _expect(self, "q", q, (self.cfg.batch, None, self.cfg.head_dim), self.torch.float16)
         hq = q.shape[1]
-        if hq not in self._window_ws:
+        ws = self._window_ws.get(hq)
+        if ws is None:
             nbytes = kivi_window_workspace_bytes(self.cfg, hq)
             if nbytes == 0:
                 raise KiviError(1, "kivi_window_workspace_bytes")
-            self._window_ws[hq] = _Workspace(self, nbytes, stream)
-        ws = self._window_ws[hq]
+            ws = self._window_ws[hq] = _Workspace(self, nbytes, stream)
         out = _output(self, out, q, stream)
         scale = 1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale
-        with self.torch.cuda.device(self.device):
+        with _on(self):
             kivi_decode_attention_window(self.cfg, self.c, q.data_ptr(), hq, scale, _int32("window", window),
-                                         _int32("sinks", sinks), out.data_ptr(),
-                                         ws.ptr, ws.nbytes, self.status.data_ptr() if status else None,
-                                         self._stream(stream))
+                                         _int32("sinks", sinks), out.data_ptr(), ws.ptr, ws.nbytes,
+                                         self.status.data_ptr() if status else None, _raw_stream(self, stream))
         return out
 
     def step_rotary(self, rotary: "Rotary", k_new, v_new, q, q_weight=None, k_weight=None, eps: float = 1e-6, out=None,
@@ -443,12 +447,39 @@ class KiviCache:
 def _expect(owner, name: str, t, shape, dtype, contiguous: bool = True) -> None:
     """Raises ValueError unless t is a tensor of that dtype and shape (None: any extent) on the owner's
     device, dense unless contiguous is False."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != g for g, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: want {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or (owner.device.index is not None and t.device.index != owner.device.index):
-        raise ValueError(f"{name}: on {t.device}, the cache is on {owner.device}")
+    got = t.shape
+    ok = t.dtype is dtype and len(got) == len(shape)
+    if ok:
+        for want, n in zip(shape, got):
+            if want is not None and want != n:
+                ok = False
+    if not ok:
+        raise ValueError(f"{name}: want {dtype} {list(shape)}, got {t.dtype} {list(got)}")
+    if not t.is_cuda or t.get_device() != owner.index:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {owner.status.device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
+
+
+def _raw_stream(owner, stream) -> int:
+    """The handle of `stream`, or of the owner's device's current stream."""
+    return stream.cuda_stream if stream is not None else owner.torch._C._cuda_getCurrentRawStream(owner.index)
+
+
+class _Same:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_SAME = _Same()
+
+
+def _on(owner):
+    """A context on the owner's device, for free where it is the current one."""
+    return _SAME if owner.index == owner.torch._C._cuda_getDevice() else owner.torch.cuda.device(owner.index)
 
 
 def _int32(name: str, x: int) -> int:
@@ -504,40 +535,38 @@ class Rotary:
         self.c = kivi_rotary_init(rotary_dim, 1 if interleaved else 0, theta, ROPE_SCALINGS[scaling], factor, low, high,
                                   original_positions)
 
-    def _heads(self, name: str, x, y, weight, like, stream):
-        """kivi_heads of x ([tokens][heads][128], or [B][heads][T][128] as the cache's prefill takes it)
-        and the output tensor."""
+    def _heads(self, name: str, x, y, weight, like, stream) -> tuple:
+        """The bytes of kivi_heads of x ([tokens][heads][128], or [B][heads][T][128] as the cache's prefill
+        takes it) and the output tensor."""
         torch = self.torch
-        if x.dtype != like.dtype or x.device != like.device or x.dim() != like.dim() or x.shape[-1] != 128:
-            raise ValueError(f"{name}: {x.dtype} {list(x.shape)} on {x.device} does not go with "
-                             f"{like.dtype} {list(like.shape)} on {like.device}")
-        four = x.dim() == 4
-        rows = (x.shape[0], x.shape[2]) if four else x.shape[:1]
-        if rows != ((like.shape[0], like.shape[2]) if four else like.shape[:1]):
-            raise ValueError(f"{name}: {list(x.shape)} has other tokens than {list(like.shape)}")
+        shape, wanted = x.shape, like.shape
+        n = len(shape)
+        if x is not like and (x.dtype is not like.dtype or not x.is_cuda or x.get_device() != like.get_device() or n != len(wanted)
+                              or shape[0] != wanted[0] or (n == 4 and shape[2] != wanted[2])):
+            raise ValueError(f"{name}: {x.dtype} {list(shape)} on {x.device} does not go with {like.dtype} {list(wanted)} on {like.device}")
+        if shape[-1] != 128:
+            raise ValueError(f"{name}: heads of {shape[-1]} channels, want 128")
         if y is None:
             if stream is None:
-                y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
+                y = x.new_empty(shape, dtype=torch.float16)
             else:
                 with torch.cuda.stream(stream):
-                    y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
-        elif y.dtype != torch.float16 or y.shape != x.shape or y.device != x.device:
-            raise ValueError(f"{name} output: want float16 {list(x.shape)} on {x.device}")
+                    y = x.new_empty(shape, dtype=torch.float16)
+        elif y.dtype is not torch.float16 or y.shape != shape or y.device != x.device:
+            raise ValueError(f"{name} output: want float16 {list(shape)} on {x.device}")
         sx, sy = x.stride(), y.stride()
         if sx[-1] != 1 or sy[-1] != 1:
             raise ValueError(f"{name}: channels must be contiguous")
-        if any(n > 1 and s == 0 for n, s in zip(y.shape, sy)):
+        if 0 in sy and any(m > 1 and s == 0 for m, s in zip(shape, sy)):
             raise ValueError(f"{name} output: expanded dimensions share memory")
-        if weight is not None and (weight.dtype != x.dtype or weight.shape != (128,) or weight.device != x.device
-                                   or not weight.is_contiguous()):
-            raise ValueError(f"{name} weight: want contiguous {x.dtype} [128] on {x.device}")
-        w = None if weight is None else weight.data_ptr()
-        if four:
-            b, h, t = 0, 1, 2
-            st = (sx[b], sx[t], sx[h], sy[b], sy[t], sy[h])
-        else:
-            st = (0, sx[0], sx[1], 0, sy[0], sy[1])
-        return kivi_heads(x.data_ptr(), y.data_ptr(), w, x.shape[1], 0, *st), y
+        w = 0
+        if weight is not None:
+            if weight.dtype is not x.dtype or weight.shape != (128,) or weight.device != x.device or not weight.is_contiguous():
+                raise ValueError(f"{name} weight: want contiguous {x.dtype} [128] on {x.device}")
+            w = weight.data_ptr()
+        if n == 4:
+            return _HEADS.pack(x.data_ptr(), y.data_ptr(), w, shape[1], 0, sx[0], sx[2], sx[1], sy[0], sy[2], sy[1]), y
+        return _HEADS.pack(x.data_ptr(), y.data_ptr(), w, shape[1], 0, 0, sx[0], sx[1], 0, sy[0], sy[1]), y
 
     def apply(self, q, k, v=None, positions=0, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
               v_out=None, stream=None):
@@ -547,8 +576,9 @@ class Rotary:
         positions: int32 device tensor of one entry per token ([tokens] or [B][T]), or the first position.
         Outputs may be given; an fp16 input may be its own output."""
         torch = self.torch
-        dtypes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
-        if q.dtype not in dtypes or not q.is_cuda or q.dim() not in (3, 4):
+        dtype = DTYPE_F16 if q.dtype is torch.float16 else DTYPE_BF16
+        n = q.dim()
+        if (dtype == DTYPE_BF16 and q.dtype is not torch.bfloat16) or not q.is_cuda or n not in (3, 4):
             raise ValueError(f"q: want fp16 or bf16 [tokens][heads][128] or [B][heads][T][128] on the GPU, "
                              f"got {q.dtype} {list(q.shape)} on {q.device}")
         hq, q_out = self._heads("q", q, q_out, q_weight, q, stream)
@@ -556,22 +586,23 @@ class Rotary:
         hv = None
         if v is not None:
             hv, v_out = self._heads("v", v, v_out, None, q, stream)
-        batch, tokens = (q.shape[0], q.shape[2]) if q.dim() == 4 else (1, q.shape[0])
+        batch, tokens = (q.shape[0], q.shape[2]) if n == 4 else (1, q.shape[0])
         if isinstance(positions, int):
             ptr, first = None, _int32("positions", positions)
         else:
-            if positions.dtype != torch.int32 or positions.numel() != batch * tokens or not positions.is_contiguous() \
+            if positions.dtype is not torch.int32 or positions.numel() != batch * tokens or not positions.is_contiguous() \
                     or positions.device != q.device:
                 raise ValueError(f"positions: want contiguous int32 of {batch * tokens} entries on {q.device}")
             ptr, first = positions.data_ptr(), 0
         if batch * tokens == 0:
             return q_out, k_out, v_out
-        s = stream if stream is not None else torch.cuda.current_stream(q.device)
-        if q.device.index != torch.cuda.current_device():
-            with torch.cuda.device(q.device):
-                kivi_rotary_apply(self.c, dtypes[q.dtype], batch, tokens, ptr, first, hq, hk, hv, eps, s.cuda_stream)
+        index = q.get_device()
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+        if index == torch._C._cuda_getDevice():
+            kivi_rotary_apply(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
         else:
-            kivi_rotary_apply(self.c, dtypes[q.dtype], batch, tokens, ptr, first, hq, hk, hv, eps, s.cuda_stream)
+            with torch.cuda.device(index):
+                kivi_rotary_apply(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
         return q_out, k_out, v_out
 
 
@@ -627,6 +658,7 @@ class PagedKiviCache:
         self.view("free_pages").copy_(torch.arange(num_pages, dtype=torch.int32))
         self.view("queue").copy_(torch.tensor([0, num_pages]))
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self.index = self.status.device.index
         self._ws = {}
         if num_q_heads is not None:
             self._workspace(num_q_heads, None)
@@ -640,14 +672,8 @@ class PagedKiviCache:
             ws = self._ws[num_q_heads] = _Workspace(self, nbytes, stream)
         return ws
 
-    def _stream(self, stream) -> int:
-        return (stream if stream is not None else self.torch.cuda.current_stream(self.device)).cuda_stream
-
     def _call(self, fn, *args) -> None:
-        if self.device.index != self.torch.cuda.current_device():
-            with self.torch.cuda.device(self.device):
-                fn(self.cfg, self.c, *args)
-        else:
+        with _on(self):
             fn(self.cfg, self.c, *args)
 
     def view(self, name: str):
@@ -682,7 +708,7 @@ class PagedKiviCache:
         self._call(kivi_paged_build_tables, lens.shape[0], lens.data_ptr(), new_tokens.data_ptr(),
                    (lens if lens_out is None else lens_out).data_ptr(),
                    self.c.queue if queue_out is None else queue_out.data_ptr(), plan.c,
-                   self.status.data_ptr() if status else None, self._stream(stream))
+                   self.status.data_ptr() if status else None, _raw_stream(self, stream))
 
     def append(self, plan: PagedPlan, k, v, stream=None, status: bool = True) -> None:
         """Writes a step's tokens (kivi_paged_append): k, v fp16 [tokens][H][128] of equal strides that keep
@@ -699,7 +725,7 @@ class PagedKiviCache:
         if k.shape[0] < plan.max_tokens:  # a plan of more tokens than there are rows must not read past them
             c = kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, k.shape[0], c.max_runs)
         self._call(kivi_paged_append, c, k.data_ptr(), v.data_ptr(), sk[0], sk[1],
-                   self.status.data_ptr() if status else None, self._stream(stream))
+                   self.status.data_ptr() if status else None, _raw_stream(self, stream))
 
     def attend(self, lens, q, plan: PagedPlan | None = None, out=None, scale: float | None = None, window: int = 0,
                sinks: int = 0, stream=None, status: bool = True):
@@ -719,7 +745,7 @@ class PagedKiviCache:
                    None if plan is None else plan.c.cu_tokens, q.data_ptr(), q.shape[0], q.shape[1],
                    1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
                    _int32("sinks", sinks), out.data_ptr(), ws.ptr,
-                   ws.nbytes, self.status.data_ptr() if status else None, self._stream(stream))
+                   ws.nbytes, self.status.data_ptr() if status else None, _raw_stream(self, stream))
         return out
 
     def step(self, plan: PagedPlan, lens, new_tokens, q, k, v, rotary: Rotary | None = None, q_weight=None, k_weight=None,
@@ -743,4 +769,4 @@ class PagedKiviCache:
                            status=status)
 
     def read_status(self, stream=None) -> int:
-        return kivi_read_status(self.status.data_ptr(), self._stream(stream))
+        return kivi_read_status(self.status.data_ptr(), _raw_stream(self, stream))
