@@ -1,10 +1,10 @@
 // Norms of queries and keys per head with the position rotation, in one pass, rounded once to the
 // fp16 the cache holds.
 //
-// One memory pass (2 bytes read and written per element) bounds it.  A CTA takes a few tokens: its
-// threads first work out the tokens' cosines and sines, one per (token, pair), into shared memory;
-// then 8 lanes hold one head row (two 16-byte chunks each, chosen so that a pair's two channels are in
-// the same lane for every layout) and a warp passes over 4 head rows at a time.
+// One memory pass (2 bytes read and written per element) bounds it.  A warp takes a token and its heads, four head rows at a
+// time: 8 lanes hold one head row (two 16-byte chunks each, chosen so that a pair's two channels are in the same lane for every
+// layout), and the rows of the next four steps are on their way to shared memory meanwhile.  The token's cosines and sines are formed once, two pairs a lane,
+// and stay in registers with the norm's weights multiplied in, four factors a pair.
 //
 // The angle is exact: turns[i] is a pair's frequency in turns per position as a 64-bit fraction, so
 // position * turns[i] modulo 2^64 is the fraction of a turn without any rounding (a float32 product
@@ -21,7 +21,9 @@ namespace kivi {
 namespace {
 
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryTokens = 4;  // tokens a CTA holds cosines for: one (token, pair) per thread
+constexpr int kRotaryWarps = kRotaryThreads / 32;
+constexpr int kRowsAtOnce = 4;  // head rows a warp holds
+constexpr int kDepth = 4;       // steps whose rows are on their way
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -42,6 +44,10 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -52,117 +58,130 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// grid: x = groups of `per_cta` tokens, y = shares of the heads
-template <bool BF16>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int per_cta) {
-  __shared__ __align__(16) float2 cs[kRotaryTokens][kHeadDim / 2];
-  const int tid = threadIdx.x;
-  const unsigned rows = static_cast<unsigned>(a.batch) * a.tokens;  // below 2^31
-  const unsigned t0 = blockIdx.x * per_cta;
-  const int nt = min(per_cta, static_cast<int>(rows - t0));
-  const int pairs = a.rotary_dim / 2;
-  {
-    const int t = tid >> 6, i = tid & 63;
-    if (t < nt && i < pairs) {
-      const unsigned row = t0 + t;
-      const int pos = a.positions != nullptr ? a.positions[row] : a.position0 + static_cast<int>(row % static_cast<unsigned>(a.tokens));
+// grid: x = groups of 8 tokens, y = shares of `share` heads of all kinds
+template <bool BF16, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRotaryThreads, 3) rotary_kernel(const __grid_constant__ RotaryArgs a, int share) {
+  __shared__ __align__(16) float2 cs[kRotaryWarps][kHeadDim / 2];
+  __shared__ uint4 ring[kRotaryWarps][kDepth][2][32];  // a lane's two chunks of the head rows on their way
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned row = blockIdx.x * kRotaryWarps + warp;
+  if (row >= static_cast<unsigned>(a.batch) * a.tokens) return;  // below 2^31
+  const unsigned bu = a.batch == 1 ? 0u : row / static_cast<unsigned>(a.tokens);
+  const long long b = bu, ti = row - bu * static_cast<unsigned>(a.tokens);
+  const int j = lane & 7, slot = lane >> 3;
+  const int pairs = a.rotary_dim / 2, rot = a.rotary_dim / 16;  // lanes j < rot hold pairs 8 j .. 8 j + 7
+  // chunks of 8 channels: the two halves of 8 pairs (half layout), or 8 pairs side by side
+  const bool apart = !INTERLEAVED && j < rot;
+  const int ca = apart ? j : 2 * j, cb = apart ? j + rot : 2 * j + 1;
+  const int h1 = min(a.heads, static_cast<int>(blockIdx.y + 1) * share);
+  int h = static_cast<int>(blockIdx.y) * share + slot;
+
+  auto kind_of = [&](int at) { return at < a.h[0].heads ? 0 : (at < a.h[0].heads + a.h[1].heads ? 1 : 2); };
+  auto index_of = [&](int at, int kind) -> long long {
+    return at - (kind > 0 ? a.h[0].heads : 0) - (kind > 1 ? a.h[1].heads : 0);
+  };
+  const uint32_t mine = smem_u32(&ring[warp][0][0][lane]);
+  int ahead = h, put = 0;  // the head row that is fetched next, and its place in the ring
+  auto fetch = [&]() {
+    if (ahead < h1) {
+      const int kind = kind_of(ahead);
+      const RotaryHeads& k = a.h[kind];
+      const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(k.x) + b * k.x_batch + ti * k.x_token +
+                                                      index_of(ahead, kind) * k.x_head);
+      copy16(mine + put * 1024, x + ca);
+      copy16(mine + put * 1024 + 512, x + cb);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += kRowsAtOnce;
+    put = put + 1 == kDepth ? 0 : put + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * lane + e;
+    if (i < pairs) {
+      const int pos = a.positions != nullptr ? a.positions[row] : a.position0 + static_cast<int>(ti);
       const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(pos)) * a.turns[i];
       float s, c;
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
-      cs[t][i] = make_float2(a.magnitude * c, a.magnitude * s);
+      // vector (i / 2) % 4 of lane i / 8: lanes read neighbouring vectors
+      cs[warp][2 * (8 * ((i >> 1) & 3) + (i >> 3)) + (i & 1)] = make_float2(a.magnitude * c, a.magnitude * s);
     }
   }
-  __syncthreads();
-  const int j = tid & 7;         // lane of the head row's 8
-  const int slot = tid >> 3;     // head row of the CTA's 32
-  const int rot = a.rotary_dim / 16;  // lanes whose chunks rotate
-  // chunks of 8 channels: the two halves of 8 pairs (half layout), or 8 pairs side by side
-  int ca, cb;
-  if (a.interleaved || j >= rot) {
-    ca = 2 * j;
-    cb = 2 * j + 1;
-  } else {
-    ca = j;
-    cb = j + rot;
-  }
-  const int items = nt * a.heads;
-  const int stride = (kRotaryThreads / 8) * gridDim.y;
-  for (int it0 = blockIdx.y * (kRotaryThreads / 8); it0 < items; it0 += stride) {
-    const int it = it0 + slot;
-    const bool live = it < items;
-    const int t = live ? it / a.heads : 0;
-    int h = live ? it - t * a.heads : 0;
-    int kind = 0;
-    if (h >= a.h[0].heads) {
-      h -= a.h[0].heads;
-      kind = 1;
-      if (h >= a.h[1].heads) {
-        h -= a.h[1].heads;
-        kind = 2;
+  __syncwarp();
+  // first element a, second element b of pair p: a' = a fa - b fb, b' = a ga + b gb; no pair: a' = a fa, b' = b gb
+  float fa[8], fb[8], ga[8], gb[8];
+  int kind = -1;
+  const int steps = (h1 - static_cast<int>(blockIdx.y) * share + kRowsAtOnce - 1) / kRowsAtOnce;
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    const bool live = h < h1;
+    const int now = live ? kind_of(h) : kind;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");  // a lane reads what it has copied itself
+    const uint4 va = ring[warp][put][0][lane], vb = ring[warp][put][1][lane];
+    fetch();
+    if (live && now != kind) {  // another kind of heads: its factors
+      kind = now;
+      const uint4* w = static_cast<const uint4*>(a.h[kind].weight);
+      float wa[8], wb[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
+      if (w != nullptr) {
+        unpack8<BF16>(__ldg(w + ca), wa);
+        unpack8<BF16>(__ldg(w + cb), wb);
+      }
+      const float4* c4 = reinterpret_cast<const float4*>(cs[warp]) + j;
+#pragma unroll
+      for (int p = 0; p < 8; p += 2) {
+        float4 u = make_float4(1.f, 0.f, 1.f, 0.f);  // (cos, sin) of two pairs
+        if (a.h[kind].rotate && j < rot) u = c4[4 * p];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int q = p + e;
+          const float w0 = INTERLEAVED ? (q < 4 ? wa[2 * q] : wb[2 * q - 8]) : wa[q];
+          const float w1 = INTERLEAVED ? (q < 4 ? wa[2 * q + 1] : wb[2 * q - 7]) : wb[q];
+          const float c = e ? u.z : u.x, s = e ? u.w : u.y;
+          fa[q] = w0 * c;
+          fb[q] = w1 * s;
+          ga[q] = w0 * s;
+          gb[q] = w1 * c;
+        }
       }
     }
-    const RotaryHeads& k = a.h[kind];
-    const unsigned row = t0 + t, bu = a.batch == 1 ? 0u : row / static_cast<unsigned>(a.tokens);
-    const long long b = bu, ti = row - bu * static_cast<unsigned>(a.tokens);
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(k.x) + b * k.x_batch + ti * k.x_token +
-                                                    h * k.x_head);
-    uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-    if (live) {
-      va = x[ca];
-      vb = x[cb];
-    }
-    float fa[8], fb[8];
-    unpack8<BF16>(va, fa);
-    unpack8<BF16>(vb, fb);
+    float xa[8], xb[8];
+    unpack8<BF16>(va, xa);
+    unpack8<BF16>(vb, xb);
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += fa[i] * fa[i] + fb[i] * fb[i];
+    for (int i = 0; i < 8; ++i) sum += xa[i] * xa[i] + xb[i] * xb[i];
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (!live) continue;
-    if (k.weight != nullptr) {
-      const float r = rsqrtf(sum * (1.0f / kHeadDim) + a.eps);
-      const uint4* w = static_cast<const uint4*>(k.weight);
-      float wa[8], wb[8];
-      unpack8<BF16>(__ldg(w + ca), wa);
-      unpack8<BF16>(__ldg(w + cb), wb);
+    if (live) {
+      if (a.h[kind].weight != nullptr) {
+        const float f = rsqrtf(sum * (1.0f / kHeadDim) + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        fa[i] *= r * wa[i];
-        fb[i] *= r * wb[i];
-      }
-    }
-    if (k.rotate && j < rot) {
-      const float4* c4 = reinterpret_cast<const float4*>(&cs[t][8 * j]);
-      if (a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float4 p = c4[i / 2], q = c4[2 + i / 2];  // (cos, sin) of two pairs each
-          const float a0 = fa[2 * i], a1 = fa[2 * i + 2], b0 = fb[2 * i], b1 = fb[2 * i + 2];
-          fa[2 * i] = a0 * p.x - fa[2 * i + 1] * p.y;
-          fa[2 * i + 1] = a0 * p.y + fa[2 * i + 1] * p.x;
-          fa[2 * i + 2] = a1 * p.z - fa[2 * i + 3] * p.w;
-          fa[2 * i + 3] = a1 * p.w + fa[2 * i + 3] * p.z;
-          fb[2 * i] = b0 * q.x - fb[2 * i + 1] * q.y;
-          fb[2 * i + 1] = b0 * q.y + fb[2 * i + 1] * q.x;
-          fb[2 * i + 2] = b1 * q.z - fb[2 * i + 3] * q.w;
-          fb[2 * i + 3] = b1 * q.w + fb[2 * i + 3] * q.z;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float4 p = c4[i / 2];
-          const float a0 = fa[i], a1 = fa[i + 1];
-          fa[i] = a0 * p.x - fb[i] * p.y;
-          fb[i] = a0 * p.y + fb[i] * p.x;
-          fa[i + 1] = a1 * p.z - fb[i + 1] * p.w;
-          fb[i + 1] = a1 * p.w + fb[i + 1] * p.z;
+        for (int i = 0; i < 8; ++i) {
+          xa[i] *= f;
+          xb[i] *= f;
         }
       }
+      const bool turned = a.h[kind].rotate && j < rot;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float& x0 = INTERLEAVED ? (q < 4 ? xa[2 * q] : xb[2 * q - 8]) : xa[q];
+        float& x1 = INTERLEAVED ? (q < 4 ? xa[2 * q + 1] : xb[2 * q - 7]) : xb[q];
+        const float y0 = x0 * fa[q], y1 = x1 * gb[q];  // an infinite element without a partner stays by itself
+        const float z0 = turned ? fmaf(-x1, fb[q], y0) : y0;
+        x1 = turned ? fmaf(x0, ga[q], y1) : y1;
+        x0 = z0;
+      }
+      const RotaryHeads& k = a.h[kind];
+      uint4* y = reinterpret_cast<uint4*>(k.y + b * k.y_batch + ti * k.y_token + index_of(h, kind) * k.y_head);
+      y[ca] = pack8(xa);
+      y[cb] = pack8(xb);
     }
-    uint4* y = reinterpret_cast<uint4*>(k.y + b * k.y_batch + ti * k.y_token + h * k.y_head);
-    y[ca] = pack8(fa);
-    y[cb] = pack8(fb);
+    h += kRowsAtOnce;
   }
 }
 
@@ -171,14 +190,25 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.batch) * a.tokens;
   if (rows == 0 || a.heads == 0) return cudaSuccess;
-  // few tokens: one per CTA and the heads split, so that a decode step's rows are all in flight at once
-  const bool few = rows < 4 * 148;
-  const int per_cta = few ? 1 : kRotaryTokens;
-  dim3 grid(static_cast<unsigned>((rows + per_cta - 1) / per_cta), few ? (a.heads + 31) / 32 : 1);
-  if (dtype == KIVI_DTYPE_BF16)
-    rotary_kernel<true><<<grid, kRotaryThreads, 0, stream>>>(a, per_cta);
-  else
-    rotary_kernel<false><<<grid, kRotaryThreads, 0, stream>>>(a, per_cta);
+  // a warp takes all heads of a token where that fills the GPU (16 warps an SM); else the heads are shared out, down to four a
+  // warp, so that a decode step's rows are all in flight at once
+  const long long want = 148ll * 16;
+  long long share = (a.heads * rows + want - 1) / want;
+  share = (share + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce;
+  if (share > a.heads) share = a.heads;
+  const dim3 grid(static_cast<unsigned>((rows + kRotaryWarps - 1) / kRotaryWarps), static_cast<unsigned>((a.heads + share - 1) / share));
+  const int n = static_cast<int>(share);
+  if (dtype == KIVI_DTYPE_BF16) {
+    if (a.interleaved)
+      rotary_kernel<true, true><<<grid, kRotaryThreads, 0, stream>>>(a, n);
+    else
+      rotary_kernel<true, false><<<grid, kRotaryThreads, 0, stream>>>(a, n);
+  } else {
+    if (a.interleaved)
+      rotary_kernel<false, true><<<grid, kRotaryThreads, 0, stream>>>(a, n);
+    else
+      rotary_kernel<false, false><<<grid, kRotaryThreads, 0, stream>>>(a, n);
+  }
   return cudaGetLastError();
 }
 
