@@ -461,6 +461,13 @@ def _expect(owner, name: str, t, shape, dtype, contiguous: bool = True) -> None:
         raise ValueError(f"{name}: not contiguous")
 
 
+def _vector(owner, name: str, t, n, dtype) -> None:
+    """_expect of one dimension (n None: any extent)."""
+    if not (t.dtype is dtype and t.dim() == 1 and (n is None or t.shape[0] == n) and t.get_device() == owner.index
+            and t.is_contiguous()):
+        _expect(owner, name, t, (n,), dtype)
+
+
 def _raw_stream(owner, stream) -> int:
     """The handle of `stream`, or of the owner's device's current stream."""
     return stream.cuda_stream if stream is not None else owner.torch._C._cuda_getCurrentRawStream(owner.index)
@@ -548,10 +555,10 @@ class Rotary:
             raise ValueError(f"{name}: heads of {shape[-1]} channels, want 128")
         if y is None:
             if stream is None:
-                y = x.new_empty(shape, dtype=torch.float16)
+                y = torch.empty_like(x, dtype=torch.float16, memory_format=torch.contiguous_format)
             else:
                 with torch.cuda.stream(stream):
-                    y = x.new_empty(shape, dtype=torch.float16)
+                    y = torch.empty_like(x, dtype=torch.float16, memory_format=torch.contiguous_format)
         elif y.dtype is not torch.float16 or y.shape != shape or y.device != x.device:
             raise ValueError(f"{name} output: want float16 {list(shape)} on {x.device}")
         sx, sy = x.stride(), y.stride()
@@ -598,11 +605,13 @@ class Rotary:
             return q_out, k_out, v_out
         index = q.get_device()
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+        call = load_library().kivi_rotary_apply
         if index == torch._C._cuda_getDevice():
-            kivi_rotary_apply(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
+            st = call(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
         else:
             with torch.cuda.device(index):
-                kivi_rotary_apply(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
+                st = call(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
+        _check(st, "kivi_rotary_apply")
         return q_out, k_out, v_out
 
 
@@ -698,14 +707,14 @@ class PagedKiviCache:
                      status: bool = True) -> None:
         """Tables of a step (kivi_paged_build_tables): lens, new_tokens int32 [n], n <= num_seqs.  The new
         lengths and queue replace the old ones unless lens_out (int32 [n]) or queue_out (int64 [2]) take them."""
-        i32 = self.torch.int32
-        _expect(self, "lens", lens, (None,), i32)
-        _expect(self, "new_tokens", new_tokens, lens.shape, i32)
+        i32, n = self.torch.int32, lens.shape[0] if lens.dim() == 1 else None
+        _vector(self, "lens", lens, n, i32)
+        _vector(self, "new_tokens", new_tokens, n, i32)
         if lens_out is not None:
-            _expect(self, "lens_out", lens_out, lens.shape, i32)
+            _vector(self, "lens_out", lens_out, n, i32)
         if queue_out is not None:
-            _expect(self, "queue_out", queue_out, (2,), self.torch.int64)
-        self._call(kivi_paged_build_tables, lens.shape[0], lens.data_ptr(), new_tokens.data_ptr(),
+            _vector(self, "queue_out", queue_out, 2, self.torch.int64)
+        self._call(kivi_paged_build_tables, n, lens.data_ptr(), new_tokens.data_ptr(),
                    (lens if lens_out is None else lens_out).data_ptr(),
                    self.c.queue if queue_out is None else queue_out.data_ptr(), plan.c,
                    self.status.data_ptr() if status else None, _raw_stream(self, stream))
@@ -733,7 +742,7 @@ class PagedKiviCache:
         fp16 [rows][Hq][128].  Without a plan row i is sequence i; with one, q holds a row per new token of
         the step and only the last of each sequence is attended (other rows of out stay as they are, so
         give `out` or do not read them)."""
-        _expect(self, "lens", lens, (None,), self.torch.int32)
+        _vector(self, "lens", lens, None, self.torch.int32)
         _expect(self, "q", q, (None, None, self.cfg.head_dim), self.torch.float16)
         if plan is None and q.shape[0] < lens.shape[0]:
             raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
