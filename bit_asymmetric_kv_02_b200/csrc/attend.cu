@@ -673,6 +673,9 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   static constexpr int HP = P / 2;                  // code pairs per word
   static constexpr int MT = UT / 16;                // K tiles per unit
   static constexpr int KW = kHeadDim / P / 4;       // K words per lane and token
+  // At 4 bits the V codes are all put at bits 4..7 of their halves (code 2^-20): products of the smallest subnormals lose their
+  // last bits, which shows where sum_t p_t z takes most of the sum back (0.00025 -> 0.00021 of the output at 8000 tokens).
+  static constexpr int kVUp = BITS == 4 ? 4 : 0;
   struct Res {
     float p[NB][2], r[NB][8][4];
   };
@@ -682,7 +685,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   float m[NB], thr[NB], l[NB], Z[NB], o[NB][8][4];
   float qs[NB][4];   // scale * log2 e * sum of q over channels 32 i .. 32 i + 31
   int qe[NB];        // exponent of the largest |q|
-  int eref;          // exponent field of the largest V scale so far: o carries 2^-eref (P operands 2^(24 - eref))
+  int eref;          // exponent field of the largest V scale so far: o carries 2^(kVUp - eref) (P operands 2^(24 - eref))
 
   using Base::Base;
 
@@ -894,7 +897,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         fac[tb][0] = s * pow2i(-2 * jl);
         fac[tb][1] = s * (jl == 0 ? 0x1p-8f : pow2i(2 - 2 * jl));
       } else {
-        fac[tb][0] = (jl & 1) ? s * 0x1p-4f : s;
+        fac[tb][0] = s;
       }
     }
     constexpr int HALF = MT / 2;  // tiles of one tb
@@ -944,48 +947,51 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
           pb[b][jl][0] = x.x, pb[b][jl][1] = x.y;
         }
       }
+    // The sums of a unit start from zero and join o by rounded additions: the tensor cores cut sums off, and over a long
+    // sequence of positive terms, most of which sum_t p_t z then takes back, that would show.
     const uint8_t* vt = S.v + t * kVPieceStride + 64 * g;
-    if constexpr (BITS == 2) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          uint32_t up[4];
+      for (int x = 0; x < 2; ++x) {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
+        w[x][0] = w4.x, w[x][1] = w4.y, w[x][2] = w4.z, w[x][3] = w4.w;
+      }
+      float c[2][NB][4];
+      auto product = [&](bool first, int e, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, int jl, int x) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up[e] = upper_codes<BITS>(w[e]);
+        for (int b = 0; b < NB; ++b) {
+          if (first)
+            mma16_first(c[e / 2][b], a0, a1, a2, a3, pb[b][jl][2 * x], pb[b][jl][2 * x + 1]);
+          else
+            mma16(c[e / 2][b], a0, a1, a2, a3, pb[b][jl][2 * x], pb[b][jl][2 * x + 1]);
+        }
+      };
 #pragma unroll
-          for (int jl = 0; jl < 4; ++jl)
+      for (int jl = 0; jl < 4; ++jl) {
+        if constexpr (BITS == 2) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const uint32_t a0 = code_pair<BITS>(w[e], up[e], jl), a1 = code_pair<BITS>(w[e + 1], up[e + 1], jl);
-              const uint32_t a2 = code_pair<BITS>(w[e], up[e], jl + 4), a3 = code_pair<BITS>(w[e + 1], up[e + 1], jl + 4);
-#pragma unroll
-              for (int b = 0; b < NB; ++b) mma16(o[b][2 * i + e / 2], a0, a1, a2, a3, pb[b][jl][2 * x], pb[b][jl][2 * x + 1]);
+              const uint32_t v0 = w[x][e], v1 = w[x][e + 1], u0 = upper_codes<2>(v0), u1 = upper_codes<2>(v1);
+              product(jl == 0 && x == 0, e, code_pair<2>(v0, u0, jl), code_pair<2>(v1, u1, jl), code_pair<2>(v0, u0, jl + 4),
+                      code_pair<2>(v1, u1, jl + 4), jl, x);
             }
+        } else {
+          auto pair = [&](uint32_t v) { return (jl == 0 ? v * 16u : (jl == 1 ? v : v >> (jl == 2 ? 4 : 8))) & 0x00F000F0u; };
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            product(jl == 0, e, pair(w[0][e]), pair(w[0][e + 1]), pair(w[1][e]), pair(w[1][e + 1]), jl, 0);
         }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[2][4], up[2][4];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(vt + x * 512 + 16 * i);
-          w[x][0] = w4.x, w[x][1] = w4.y, w[x][2] = w4.z, w[x][3] = w4.w;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) up[x][e] = upper_codes<BITS>(w[x][e]);
-        }
-#pragma unroll
-        for (int jl = 0; jl < 4; ++jl)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const uint32_t a0 = code_pair<BITS>(w[0][e], up[0][e], jl), a1 = code_pair<BITS>(w[0][e + 1], up[0][e + 1], jl);
-            const uint32_t a2 = code_pair<BITS>(w[1][e], up[1][e], jl), a3 = code_pair<BITS>(w[1][e + 1], up[1][e + 1], jl);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) mma16(o[b][2 * i + e / 2], a0, a1, a2, a3, pb[b][jl][0], pb[b][jl][1]);
-          }
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[b][2 * i + e][q] += c[e][b][q];
     }
   }
 
@@ -1078,7 +1084,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   __device__ __forceinline__ void res_end(Res& s) {
     const float(&r)[NB][8][4] = s.r;
     float* buf = reinterpret_cast<float*>(S.p[0]);  // 4 queries at a time of 64 channels: 1 KB
-    const float f = pow2i(-10 - eref);
+    const float f = pow2i(kVUp - 10 - eref);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -1108,7 +1114,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   // Lane (g, t): o of query t (each column block), channels 16 g .. 16 g + 15.
   __device__ __forceinline__ void finish(float* part) {
     const int nq = S.now.queries;
-    const float back = pow2i(eref);
+    const float back = pow2i(eref - kVUp);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float ls = l[b], zs = Z[b];
