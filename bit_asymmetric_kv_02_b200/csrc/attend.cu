@@ -284,6 +284,7 @@ struct __align__(128) WarpSmem {
   uint4 zero4;                        // NB == 0: the operand of the other tile of a pair
   float part[kQueries * kPart];       // of the warp's first head, where that is not whole (of its last head: in k)
   Cursor cur, now, first;             // of the unit fetched last, of the head in hand, and of the warp's first head
+  int partial;                        // bit 0: of its first head the warp has a part (in part), bit 1: of its last one (in k)
 };
 static_assert(kResTokens * kRow >= 4 * kVPieceStride && kResTokens * kRow >= kHalfBytes && kResTokens * kRow >= 8 * kPart * 4,
               "a buffer holds either kind of half, and the partials of a warp's last head");
@@ -439,9 +440,9 @@ struct Walker {
   }
 
   // ---- heads that several warps share ----------------------------------------------------------------------------
-  // Partials (m, l, Z and o[128] of each query) are joined by log-sum-exp: those of a CTA's warps in shared memory by the warp that
-  // arrives last at the head's ticket there, and those of several CTAs in global memory by the one that arrives last at the
-  // head's ticket there.  Parts are taken in their order, so the result does not depend on who arrives when.
+  // Partials (m, l, Z and o[128] of each query) are joined by log-sum-exp: those of a CTA's warps in shared memory when all of
+  // them are done, a warp per head and query, and those of several CTAs in global memory by the warp that arrives last at the
+  // ticket of the head and query.  Parts are taken in their order, so the result does not depend on who arrives when.
   struct Sums {
     float m, l, Z, o[4];  // channels 4 lane .. 4 lane + 3
   };
@@ -451,11 +452,17 @@ struct Walker {
         make_uint2(pack_h2((s.o[0] + s.Z) * inv, (s.o[1] + s.Z) * inv), pack_h2((s.o[2] + s.Z) * inv, (s.o[3] + s.Z) * inv));
   }
   // s joined with the n <= 32 parts at p0, p + stride, p + 2 stride, ..: lane i weighs part i, so that the rows follow without
-  // a chain of maxima.
+  // a chain of maxima.  GLOBAL: past the L1 cache, which may hold what was there before.
+  template <bool GLOBAL>
+  __device__ static __forceinline__ float4 part_of(const float* p) {
+    const float4* q = reinterpret_cast<const float4*>(p);
+    return GLOBAL ? __ldcg(q) : *q;
+  }
+  template <bool GLOBAL>
   __device__ static __forceinline__ void add_parts(Sums& s, int lane, const float* p0, const float* p, int stride, int n) {
-    float mi = kNoMax;
-    if (lane < n) mi = lane == 0 ? *p0 : p[lane * stride];
-    const float mn = fmaxf(s.m, max_of_warp(mi)), f = ex2(s.m - mn), w = ex2(mi - mn);
+    float4 x = make_float4(kNoMax, 0.f, 0.f, 0.f);
+    if (lane < n) x = part_of<GLOBAL>(lane == 0 ? p0 : p + lane * stride);
+    const float mn = fmaxf(s.m, max_of_warp(x.x)), f = ex2(s.m - mn), w = ex2(x.x - mn);
     s.m = mn;
     s.l *= f;
     s.Z *= f;
@@ -463,114 +470,77 @@ struct Walker {
     for (int e = 0; e < 4; ++e) s.o[e] *= f;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float* at = i == 0 ? p0 : p + i * stride;
-      const float2 x = *reinterpret_cast<const float2*>(at + 2);  // l, Z
-      const float4 v = *reinterpret_cast<const float4*>(at + 4 + 4 * lane);
+      const float4 v = part_of<GLOBAL>((i == 0 ? p0 : p + i * stride) + 4 + 4 * lane);
       const float wi = __shfl_sync(kFull, w, i);
-      s.l = fmaf(wi, x.x, s.l);
-      s.Z = fmaf(wi, x.y, s.Z);
+      s.l = fmaf(wi, __shfl_sync(kFull, x.z, i), s.l);
+      s.Z = fmaf(wi, __shfl_sync(kFull, x.w, i), s.Z);
       s.o[0] = fmaf(wi, v.x, s.o[0]);
       s.o[1] = fmaf(wi, v.y, s.o[1]);
       s.o[2] = fmaf(wi, v.z, s.o[2]);
       s.o[3] = fmaf(wi, v.w, s.o[3]);
     }
   }
-  // The warps of this CTA that hold parts of head c: first .. first + n - 1; w0 and w1 are its first and last worker.
-  struct Sharers {
-    uint32_t w0, w1;
-    int first, n;
-  };
-  __device__ static __forceinline__ Sharers sharers(const Split& sp, const Cursor& c) {
-    const uint32_t w0 = sp.worker_of(c.f0), w1 = sp.worker_of(c.f0 + c.un.total - 1), lo = blockIdx.x * sp.per_cta;
-    const uint32_t c0 = max(w0, lo), c1 = min(w1, lo + sp.per_cta - 1);
-    return {w0, w1, static_cast<int>(c0 - lo), static_cast<int>(c1 - c0) + 1};
-  }
-  // This warp's part of head c is in its shared memory: true for the last of the CTA's warps to say so, which joins them.
-  __device__ __noinline__ static bool arrive(int* tickets, const Split& sp, const Cursor& c) {
-    const Sharers h = sharers(sp, c);
-    __syncwarp();
-    if (h.n == 1) return true;
-    int last = 0;
-    if ((threadIdx.x & 31) == 0) {  // one ticket per warp: a warp is the first of one such head at most, its last one
-      __threadfence_block();
-      last = atomicAdd(tickets + h.first, 1) == h.n - 1;
-      __threadfence_block();
+  // By every warp of the CTA, behind a barrier.  The loops are kept small: this code comes from a cold instruction cache.
+  __device__ __noinline__ static void join(const AttendArgs& a, const Smem* warps, const Split& sp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, count = static_cast<int>(blockDim.x >> 5);
+    const uint32_t lo = blockIdx.x * sp.per_cta, cta_start = sp.start(min(lo, sp.workers));
+    const uint32_t cta_end = sp.start(min(lo + sp.per_cta, sp.workers));
+    // candidate 2 w + k: warp w's first (k = 0) or last head, where it has only a part of it and is the first of the CTA to
+    static_assert(2 * attend_warps<NB>() <= 32, "a lane looks at one of them");
+    bool lead = false;
+    if (lane < 2 * count) {
+      const Smem& S = warps[lane >> 1];
+      const Cursor& c = lane & 1 ? S.now : S.first;
+      lead = (S.partial >> (lane & 1) & 1) != 0 && (lane < 2 || c.f0 >= sp.start(lo + (lane >> 1)));
     }
-    return __shfl_sync(kFull, last, 0) != 0;
-  }
-  // Run once or twice per warp, mostly from a cold instruction cache: the loops are kept small, and what comes from global
-  // memory comes in one go through shared memory.  warps: the CTA's WarpSmem array.
-  __device__ __noinline__ static void join(const AttendArgs& a, Smem* warps, const Split& sp, const Cursor& c) {
-    const int lane = threadIdx.x & 31;
-    const Sharers h = sharers(sp, c);
-    const uint32_t cta = blockIdx.x, f0 = c.f0, w0 = h.w0, w1 = h.w1, c0 = cta * sp.per_cta + h.first;
-    const int first = h.first, n = h.n;
-    __syncwarp();
-    const int nq = c.queries;
-    uint16_t* out = a.out + (static_cast<size_t>(c.row) * a.heads * a.gqa + c.q0) * kHeadDim;
-    const bool whole = c0 == w0 && c0 + n - 1 == w1;
-    // only the first of the warps can have started before the head: its part is then in k
-    const float* part0 = sp.start(c0) >= f0 ? warps[first].part : reinterpret_cast<const float*>(warps[first].k);
-    // a CTA's partial heads: the one it starts in (slot 0) and the one it ends in
-    float* mine = a.partials + static_cast<size_t>(2 * cta + (sp.start(cta * sp.per_cta) >= f0 ? 0 : 1)) * NQ * kPart;
-#pragma unroll 2
-    for (int q = 0; q < nq; ++q) {
+    const unsigned leads = __ballot_sync(kFull, lead);
+    const int heads = __popc(leads);
+#pragma unroll 1
+    for (int task = warp; task < heads * a.per_pass; task += count) {
+      const int k = task / a.per_pass, q = task - k * a.per_pass;
+      unsigned rest = leads;
+      for (int i = 0; i < k; ++i) rest &= rest - 1;
+      const int at = __ffs(rest) - 1, w0 = at >> 1;
+      const Cursor& c = at & 1 ? warps[w0].now : warps[w0].first;
+      if (q >= c.queries) continue;
+      const uint32_t f0 = c.f0, f1 = f0 + c.un.total;
+      // its parts: this one, and the first heads of the warps behind it
+      const bool mine = lane >= w0 && lane < static_cast<int>(sp.per_cta) && lo + lane < sp.workers && sp.start(lo + lane) < f1;
+      const int n = __popc(__ballot_sync(kFull, mine));
+      const float* part0 = (at & 1 ? reinterpret_cast<const float*>(warps[w0].k) : warps[w0].part) + q * kPart;
       Sums s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
-      add_parts(s, lane, part0 + q * kPart, warps[first].part + q * kPart, sizeof(Smem) / sizeof(float), n);
-      if (whole) {
-        store_row(out + q * kHeadDim, lane, s);
-      } else {
-        if (lane == 0) *reinterpret_cast<float4*>(mine + q * kPart) = make_float4(s.m, 0.f, s.l, s.Z);
-        *reinterpret_cast<float4*>(mine + q * kPart + 4 + 4 * lane) = make_float4(s.o[0], s.o[1], s.o[2], s.o[3]);
+      add_parts<false>(s, lane, part0, warps[w0].part + q * kPart, sizeof(Smem) / sizeof(float), n);
+      uint16_t* out = a.out + (static_cast<size_t>(c.row) * a.heads * a.gqa + c.q0 + q) * kHeadDim;
+      if (f0 >= cta_start && f1 <= cta_end) {
+        store_row(out, lane, s);
+        continue;
       }
-    }
-    if (whole) return;
-    __syncwarp();  // every lane's share of the partial comes before the ticket
-    const uint32_t b0 = divide(w0, sp.per_cta, sp.recip_cta), b1 = divide(w1, sp.per_cta, sp.recip_cta);
-    const size_t ticket = static_cast<size_t>(c.seq) * a.heads * a.passes + c.he;
-    int last = 0;
-    if (lane == 0) last = add_acq_rel(a.tickets + ticket) == static_cast<int>(b1 - b0);
-    if (!__shfl_sync(kFull, last, 0)) return;
-    __syncwarp();
-    if (lane == 0) a.tickets[ticket] = 0;
-    const int parts = static_cast<int>(b1 - b0) + 1;
-    const float* part_0 = a.partials + (2 * static_cast<size_t>(b0) + (sp.start(b0 * sp.per_cta) >= f0 ? 0 : 1)) * NQ * kPart;
-    const float* part_i = a.partials + 2 * static_cast<size_t>(b0) * NQ * kPart;
-    // rows of partials that fit behind k (v, q, p and qh are free by now): all queries' at once, or one query's as many as fit
-    Smem& S = warps[threadIdx.x >> 5];
-    float* rows = reinterpret_cast<float*>(S.v);
-    constexpr int kRows = (sizeof(S.v) + sizeof(S.q) + sizeof(S.p) + sizeof(S.qh)) / (kPart * sizeof(float));
-    const int nb = parts * nq <= kRows ? nq : 1, np = nb == 1 ? kRows : parts;
+      // a CTA's partial heads: the one it starts in (slot 0) and the one it ends in
+      float* to = a.partials + (static_cast<size_t>(2 * blockIdx.x + (cta_start >= f0 ? 0 : 1)) * NQ + q) * kPart;
+      if (lane == 0) *reinterpret_cast<float4*>(to) = make_float4(s.m, 0.f, s.l, s.Z);
+      *reinterpret_cast<float4*>(to + 4 + 4 * lane) = make_float4(s.o[0], s.o[1], s.o[2], s.o[3]);
+      __syncwarp();  // every lane's share of the partial comes before the ticket
+      const uint32_t b0 = f0 >= cta_start ? blockIdx.x : divide(sp.worker_of(f0), sp.per_cta, sp.recip_cta);
+      const uint32_t b1 = f1 <= cta_end ? blockIdx.x : divide(sp.worker_of(f1 - 1), sp.per_cta, sp.recip_cta);
+      const size_t ticket = (static_cast<size_t>(c.seq) * a.heads * a.passes + c.he) * a.per_pass + q;
+      int last = 0;
+      if (lane == 0) last = add_acq_rel(a.tickets + ticket) == static_cast<int>(b1 - b0);
+      if (!__shfl_sync(kFull, last, 0)) continue;
+      __syncwarp();
+      if (lane == 0) a.tickets[ticket] = 0;
+      const int parts = static_cast<int>(b1 - b0) + 1, stride = 2 * NQ * kPart;
+      const float* part_i = a.partials + (2 * static_cast<size_t>(b0) * NQ + q) * kPart;
+      const float* part_0 = part_i + (sp.start(b0 * sp.per_cta) >= f0 ? 0 : NQ * kPart);
+      s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 1
-    for (int q0 = 0; q0 < nq; q0 += nb) {
-      Sums s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 1
-      for (int i0 = 0; i0 < parts; i0 += np) {
-        const int n2 = min(np, parts - i0);
-        __syncwarp();
-        uint32_t dst = smem_u32(rows) + 16 * lane;
-#pragma unroll 1
-        for (int i = i0; i < i0 + n2; ++i) {  // the rows of a part follow one another, in memory as here
-          const char* src = reinterpret_cast<const char*>((i == 0 ? part_0 : part_i + 2 * static_cast<size_t>(i) * NQ * kPart) + q0 * kPart);
-          const int bytes = nb * kPart * 4;
-#pragma unroll 2
-          for (int at = 16 * lane; at < bytes; at += 512) copy16(dst + at - 16 * lane, src + at);
-          dst += bytes;
-        }
-        copies_commit();
-        copies_wait<0>();
-#pragma unroll 1
-        for (int q = 0; q < nb; ++q) {
-          if (nb > 1) s = {kNoMax, 0.f, 0.f, {0.f, 0.f, 0.f, 0.f}};
-          add_parts(s, lane, rows + q * kPart, rows + q * kPart, nb * kPart, n2);
-          if (i0 + n2 == parts) store_row(out + (q0 + q) * kHeadDim, lane, s);
-        }
-      }
+      for (int i0 = 0; i0 < parts; i0 += 32)
+        add_parts<true>(s, lane, i0 == 0 ? part_0 : part_i + i0 * stride, part_i + i0 * stride, stride, min(32, parts - i0));
+      store_row(out, lane, s);
     }
   }
 
   // worker: of the split; seq0: row of its first unit, the row's units before it: rem.
-  __device__ __forceinline__ void run(Smem* warps, int* tickets, const Split& split, uint32_t worker, int seq0, uint32_t rem) {
+  __device__ __forceinline__ void run(const Split& split, uint32_t worker, int seq0, uint32_t rem) {
     Core& core = static_cast<Core&>(*this);
     const uint32_t f0 = split.start(worker);
     int left = static_cast<int>(split.start(worker + 1) - f0);
@@ -588,7 +558,6 @@ struct Walker {
     uint32_t kp = 0, vp = 0;
     load_pairs(kp, vp);
     uint32_t at = f0;
-    bool begun = false;  // the first head is this warp's to join, at the end: its buffers are in use until then
     while (left > 0) {
       const Cursor& c = S.cur;
       const int l0 = c.local, units = c.un.total;
@@ -653,14 +622,13 @@ struct Walker {
         core.finish(nullptr);
       } else if (at == f0) {
         core.finish(S.part);
-        begun = arrive(tickets, split, S.now);
+        if (lane == 0) S.partial |= 1;
       } else {  // the last head: no copy is in flight any more
         core.finish(reinterpret_cast<float*>(S.k));
-        if (arrive(tickets, split, S.now)) join(a, warps, split, S.now);
+        if (lane == 0) S.partial |= 2;
       }
       at += count;
     }
-    if (begun) join(a, warps, split, S.first);
   }
 };
 
@@ -1489,7 +1457,7 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   constexpr int W = attend_warps<NB>(), T = W * 32, UT = CoreOf<BITS, NB>::type::UT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = WarpSmem<BITS, NB>;
-  __shared__ int warp_sum[W], tickets[W], cum[T + 1];  // units per head before each thread's rows
+  __shared__ int warp_sum[W], cum[T + 1];  // units per head before each thread's rows
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.rows + T - 1) / T, r0 = min(a.rows, tid * per), r1 = min(a.rows, r0 + per);
   int mine = 0;
@@ -1506,7 +1474,6 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_sum[warp] = x;
-  if (lane == 0) tickets[warp] = 0;
   __syncthreads();
   int before = x - mine;
   for (int i = 0; i < warp; ++i) before += warp_sum[i];
@@ -1526,29 +1493,33 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   split.recip1 = 0xffffffffu / (split.len + 1);
   split.recip_cta = 0xffffffffu / split.per_cta;
   const uint32_t worker = blockIdx.x * split.per_cta + warp;
-  if (warp >= split.per_cta || worker >= split.workers) return;
-  // the row of the worker's first unit: its thread's rows by bisection, then one by one
-  const uint32_t f0 = split.start(worker);
-  const int want = static_cast<int>(f0 / he_count);
-  int lo = 0, hi = T;  // cum[lo] <= want < cum[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] <= want)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  int row = lo * per, first = cum[lo];
-  for (int n; first + (n = row_units<UT>(a, row)) <= want; ++row) first += n;
   Smem* warps = reinterpret_cast<Smem*>(smem_raw);
-  typename CoreOf<BITS, NB>::type d(a, warps[warp], lane);
-  d.run(warps, tickets, split, worker, row, f0 - first * he_count);
+  if (lane == 0) warps[warp].partial = 0;
+  if (warp < split.per_cta && worker < split.workers) {
+    // the row of the worker's first unit: its thread's rows by bisection, then one by one
+    const uint32_t f0 = split.start(worker);
+    const int want = static_cast<int>(f0 / he_count);
+    int lo = 0, hi = T;  // cum[lo] <= want < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= want)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    int row = lo * per, first = cum[lo];
+    for (int n; first + (n = row_units<UT>(a, row)) <= want; ++row) first += n;
+    typename CoreOf<BITS, NB>::type d(a, warps[warp], lane);
+    d.run(split, worker, row, f0 - first * he_count);
+  }
+  __syncthreads();
+  CoreOf<BITS, NB>::type::join(a, warps, split);
 }
 
 template <int BITS, int NB>
 cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
   constexpr int smem = attend_warps<NB>() * static_cast<int>(sizeof(WarpSmem<BITS, NB>));
-  static_assert(smem + 4 * (attend_warps<NB>() * 34 + 1) <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
+  static_assert(smem + 4 * (attend_warps<NB>() * 33 + 1) <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
   const cudaError_t e =
       cudaFuncSetAttribute(attend_kernel<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -1567,7 +1538,7 @@ Shape shape_of(int gqa) {
   return s;
 }
 size_t ticket_bytes(long long rows, int heads, const Shape& s) {
-  return (static_cast<size_t>(rows) * heads * s.passes * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
+  return (static_cast<size_t>(rows) * heads * s.passes * s.per_pass * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
 }
 
 }  // namespace
