@@ -7,9 +7,11 @@
 // 4 KB of K, 4 KB of V) that hold a visible token, then 16 residual rows a unit.  All units of all rows,
 // whose lengths differ, form one sequence, cut into one contiguous range per warp, so the load is even
 // whatever the lengths; every CTA finds the ranges itself from a prefix sum of the rows' unit counts.
-// A head that several warps share is joined by the warp that arrives last (its ticket), over the parts
-// in their order: results do not depend on the order of arrival, and no warp waits for another.
-// K and V halves arrive in shared memory by bulk copies, the next unit's K behind this unit's K.
+// Heads that several warps share are joined in shared memory behind the CTA's last barrier, and across CTAs by the warp that
+// arrives last at a ticket, over the parts in their order: results do not depend on the order of arrival, and no CTA waits for
+// another.
+// K and V halves arrive in shared memory by 16-byte asynchronous copies, the next unit's K behind this unit's K (bulk copies,
+// of which a warp issues one at a time, cost 200 instructions a unit in loops over the pieces).
 //
 // Products.  Both run on the tensor cores in fp16 with fp32 sums (mma m16n8k16), codes as the A operand:
 // a masked code word IS a pair of fp16 subnormals, (w & 0x0003 << 2 j) = code 4^j 2^-24, exact, so an
@@ -101,7 +103,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const char* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const char* src, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
@@ -173,7 +175,7 @@ template <int UT>
 __device__ __forceinline__ Units units_of(const Span& s) {
   Units u;
   const int nq = s.quant / UT;
-  u.q_sink = min(nq, (s.sink_end + UT - 1) / UT);
+  u.q_sink = min(nq, static_cast<int>((static_cast<uint32_t>(s.sink_end) + UT - 1) / UT));
   const int q0 = max(u.q_sink, min(nq, s.start / UT));
   u.q_gap = q0 - u.q_sink;
   u.q_units = nq - u.q_gap;
@@ -570,7 +572,7 @@ struct Walker {
       }
       __syncwarp();
       slot_now = slot;
-      full_from = (S.now.sp.start + UT - 1) / UT;
+      full_from = static_cast<int>((static_cast<uint32_t>(S.now.sp.start) + UT - 1) / UT);
       sink_full = S.now.sp.sink_end / UT;
       copies_wait<1>();  // the head's queries are here with its first K half
       core.start_head();

@@ -149,6 +149,8 @@ int kivi_decode_attention_window(const kivi_config* cfg, const kivi_cache* cache
   a.len = cache->n_quant + cache->n_res;
   a.quant = cache->n_quant;
   a.blocks_per_head = cfg->capacity / R;
+  if (static_cast<long long>(cfg->batch) * cfg->num_kv_heads > 0x7fffffffll / (a.blocks_per_head > 0 ? a.blocks_per_head : 1))
+    return KIVI_ERR_UNSUPPORTED;
   a.lg_r = log2i(R);
   a.lg_gk = log2i(cfg->group_k);
   a.lg_gv = log2i(cfg->group_v);

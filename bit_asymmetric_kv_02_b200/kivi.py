@@ -432,8 +432,10 @@ class KiviCache:
                     scale: float | None = None, stream=None, status: bool = True):
         """step() with keys and queries as the projections give them: each head normed where it has a
         weight and rotated to the new token's position (Rotary.apply), then appended and attended.
-        k_new, v_new, q: fp16 or bf16 [B][heads][128]."""
-        v = None if v_new.dtype == self.torch.float16 else v_new.unsqueeze(2)
+        k_new, v_new, q: fp16 or bf16 [B][heads][128], of any strides that keep head rows whole."""
+        for name, x, heads in (("q", q, None), ("k_new", k_new, self.cfg.num_kv_heads), ("v_new", v_new, self.cfg.num_kv_heads)):
+            _expect(self, name, x, (self.cfg.batch, heads, self.cfg.head_dim), x.dtype, contiguous=False)
+        v = None if v_new.dtype == self.torch.float16 and v_new.is_contiguous() else v_new.unsqueeze(2)
         q, k_new, v = rotary.apply(q.unsqueeze(2), k_new.unsqueeze(2), v, positions=self.n_quant + self.n_res,
                                    q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
         q, k_new, v_new = q.squeeze(2), k_new.squeeze(2), v_new if v is None else v.squeeze(2)
@@ -630,6 +632,7 @@ class PagedPlan:
         self.runs = torch.zeros(runs, 8, dtype=torch.int32, device=cache.device)
         self.counts = torch.zeros(2, dtype=torch.int32, device=cache.device)
         self.max_tokens = max_tokens
+        self.num_seqs, self.residual = cache.cfg.num_seqs, cache.cfg.residual
         self.c = kivi_paged_plan(self.cu_tokens.data_ptr(), self.positions.data_ptr(), self.runs.data_ptr(),
                                  self.counts.data_ptr(), max_tokens, runs)
 
@@ -644,28 +647,42 @@ class PagedKiviCache:
         cache.append(plan, k, v)
         out = cache.attend(lens, q, plan=plan)               # the newest token of every sequence
 
-    or all four as step().  Everything a step reads or advances is on the device, so it can be captured in a CUDA graph
-    and replayed (make one uncaptured attend() with its number of query heads first).  Calls of one cache
-    that overlap on the GPU are not allowed: they share buffers and workspaces."""
+    or all four as step().  The layers of a model share one set of tables: PagedKiviCache(..., tables=first) for
+    the others, one build_tables() a step, and append() and attend() with that plan in every layer.
+    Everything a step reads or advances is on the device, so it can be captured in a CUDA graph and replayed
+    (make one uncaptured attend() with its number of query heads first).  Calls of one cache that overlap on
+    the GPU are not allowed: they share buffers and workspaces."""
 
     def __init__(self, num_pages: int, num_seqs: int, max_blocks: int, num_kv_heads: int, bits: int = 2, group_k: int = 32,
-                 group_v: int = 32, residual: int = 128, head_dim: int = 128, num_q_heads: int | None = None, device=None):
+                 group_v: int = 32, residual: int = 128, head_dim: int = 128, num_q_heads: int | None = None, device=None,
+                 tables: "PagedKiviCache | None" = None):
         import torch
         self.torch = torch
-        self.device = torch.device(device or "cuda")
+        self.device = tables.device if tables is not None and device is None else torch.device(device or "cuda")
         self.cfg = kivi_paged_config(num_pages, num_seqs, max_blocks, num_kv_heads, head_dim, bits, group_k, group_v,
                                      residual)
         st = kivi_paged_check_config(self.cfg)
         if st != KIVI_OK:
             raise KiviError(st, "kivi_paged_check_config")
+        shared = ()
+        if tables is not None:  # a layer whose blocks lie where the other one's do
+            mine, other = self.cfg, tables.cfg
+            if (mine.num_pages, mine.num_seqs, mine.max_blocks, mine.residual) != \
+                    (other.num_pages, other.num_seqs, other.max_blocks, other.residual):
+                raise ValueError("tables: of a cache with other pages, sequences or blocks")
+            shared = PAGED_BUFFERS[len(BUFFERS):]
         self.buffers = {}
         for name, nbytes in zip(PAGED_BUFFERS, kivi_paged_sizes(self.cfg)):
-            self.buffers[name] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
-        self.device = self.buffers["queue"].device
+            self.buffers[name] = tables.buffers[name] if name in shared else \
+                torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
+        self.device = self.buffers["k_codes"].device
+        if self.device != self.buffers["queue"].device:
+            raise ValueError(f"tables: on {tables.device}, the cache on {self.device}")
         self.c = kivi_paged_cache(*[self.buffers[n].data_ptr() for n in PAGED_BUFFERS])
-        self.view("block_table").fill_(-1)
-        self.view("free_pages").copy_(torch.arange(num_pages, dtype=torch.int32))
-        self.view("queue").copy_(torch.tensor([0, num_pages]))
+        if not shared:
+            self.view("block_table").fill_(-1)
+            self.view("free_pages").copy_(torch.arange(num_pages, dtype=torch.int32))
+            self.view("queue").copy_(torch.tensor([0, num_pages]))
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self.index = self.status.device.index
         self._ws = {}
@@ -684,6 +701,10 @@ class PagedKiviCache:
     def _call(self, fn, *args) -> None:
         with _on(self):
             fn(self.cfg, self.c, *args)
+
+    def _check_plan(self, plan: PagedPlan) -> None:
+        if plan.num_seqs != self.cfg.num_seqs or plan.residual != self.cfg.residual or plan.counts.get_device() != self.index:
+            raise ValueError(f"plan: of {plan.num_seqs} sequences and {plan.residual}-token blocks on {plan.counts.device}")
 
     def view(self, name: str):
         """The buffer in the layout of include/kivi.h."""
@@ -707,6 +728,7 @@ class PagedKiviCache:
                      status: bool = True) -> None:
         """Tables of a step (kivi_paged_build_tables): lens, new_tokens int32 [n], n <= num_seqs.  The new
         lengths and queue replace the old ones unless lens_out (int32 [n]) or queue_out (int64 [2]) take them."""
+        self._check_plan(plan)
         i32, n = self.torch.int32, lens.shape[0] if lens.dim() == 1 else None
         _vector(self, "lens", lens, n, i32)
         _vector(self, "new_tokens", new_tokens, n, i32)
@@ -722,6 +744,7 @@ class PagedKiviCache:
     def append(self, plan: PagedPlan, k, v, stream=None, status: bool = True) -> None:
         """Writes a step's tokens (kivi_paged_append): k, v fp16 [tokens][H][128] of equal strides that keep
         head rows whole, tokens at least the plan's count."""
+        self._check_plan(plan)
         shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
         _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
         _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
@@ -744,7 +767,9 @@ class PagedKiviCache:
         give `out` or do not read them)."""
         _vector(self, "lens", lens, None, self.torch.int32)
         _expect(self, "q", q, (None, None, self.cfg.head_dim), self.torch.float16)
-        if plan is None and q.shape[0] < lens.shape[0]:
+        if plan is not None:
+            self._check_plan(plan)
+        elif q.shape[0] < lens.shape[0]:
             raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
         ws = self._workspace(q.shape[1], stream)
         out = _output(self, out, q, stream)
@@ -771,10 +796,13 @@ class PagedKiviCache:
                                      positions=plan.positions[:q.shape[0]], q_weight=q_weight, k_weight=k_weight, eps=eps,
                                      stream=stream)
             v = v if v16 is None else v16
-        if k.stride() != v.stride():
-            k, v = k.contiguous(), v.contiguous()
+        if k.stride() != v.stride() or not q.is_contiguous():
+            with self.torch.cuda.stream(stream):  # None: the current stream
+                if k.stride() != v.stride():
+                    k, v = k.contiguous(), v.contiguous()
+                q = q.contiguous()
         self.append(plan, k, v, stream=stream, status=status)
-        return self.attend(lens, q.contiguous(), plan=plan, out=out, scale=scale, window=window, sinks=sinks, stream=stream,
+        return self.attend(lens, q, plan=plan, out=out, scale=scale, window=window, sinks=sinks, stream=stream,
                            status=status)
 
     def read_status(self, stream=None) -> int:

@@ -612,6 +612,83 @@ def test_graph_of_steps():
             a.attend(lens_a, torch.zeros(n, H, 128, dtype=torch.float16, device="cuda"))
 
 
+def test_layers_share_tables():
+    """Two layers of other heads and bits on one set of tables: one build_tables() a step, and each layer its own data."""
+    n, g = 3, torch.Generator("cuda").manual_seed(5)
+    first = _cache(num_seqs=n, num_kv_heads=2, bits=2)
+    second = kivi.PagedKiviCache(num_pages=64, num_seqs=n, max_blocks=16, num_kv_heads=1, bits=4, group_k=128, group_v=64, tables=first)
+    assert second.view("block_table").data_ptr() == first.view("block_table").data_ptr()
+    lens, plan = _i32([0] * n), first.new_plan(900)
+    kv = {c: [(np.zeros((0, c.cfg.num_kv_heads, 128), np.float16),) * 2 for _ in range(n)] for c in (first, second)}
+    for new in ([300, 5, 127], [1, 130, 1], [1, 1, 1]):
+        first.build_tables(plan, lens, _i32(new))
+        for cache in (first, second):
+            H, at = cache.cfg.num_kv_heads, 0
+            k, v = (torch.randn(sum(new), H, 128, generator=g, device="cuda").half() for _ in range(2))
+            cache.append(plan, k, v)
+            q = torch.randn(sum(new), 4, 128, generator=g, device="cuda").half()
+            out = cache.attend(lens, q, plan=plan)
+            for i, a in enumerate(new):
+                kv[cache][i] = tuple(np.concatenate([old, y[at:at + a].cpu().numpy()]) for old, y in zip(kv[cache][i], (k, v)))
+                at += a
+            _check_cache(cache, lens.tolist(), kv[cache])
+            _check_attention(cache, cache.view("block_table").cpu().numpy(), lens.tolist(), q, out, 128 ** -0.5,
+                             rows=(np.cumsum(new) - 1).tolist())
+    with pytest.raises(ValueError):
+        kivi.PagedKiviCache(num_pages=65, num_seqs=n, max_blocks=16, num_kv_heads=1, tables=first)
+
+
+def test_append_reports_a_plan_of_more_runs_than_rows():
+    cache = _cache(num_seqs=4, num_kv_heads=1)
+    plan, lens = cache.new_plan(8), _i32([0] * 4)
+    cache.build_tables(plan, lens, _i32([1] * 4))
+    k = torch.randn(4, 1, 128, device="cuda").half()
+    cache.append(plan, k, k)
+    assert cache.read_status() == 0
+    cache.append(plan, k[:2], k[:2])
+    assert cache.read_status() == 11
+
+
+def test_pool_past_32_bits():
+    """Pages whose codes and residual rows lie past 2^32 bytes."""
+    g = torch.Generator("cuda").manual_seed(8)
+    H, pages = 16, 70000
+    cache = _cache(num_pages=pages, num_seqs=5000, max_blocks=4, num_kv_heads=H)
+    assert cache.buffers["k_codes"].numel() > 1 << 32 and cache.buffers["k_res"].numel() > 1 << 31
+    for name in kivi.BUFFERS:
+        cache.buffers[name].zero_()
+    lens = torch.zeros(5000, dtype=torch.int32, device="cuda")
+    new = torch.zeros(5000, dtype=torch.int32, device="cuda")
+    plan = cache.new_plan(600)
+    cache.view("queue").copy_(torch.tensor([pages - 4, pages]))
+    new[4999], new[17] = 260, 300
+    k, v = (torch.randn(560, H, 128, generator=g, device="cuda").half() for _ in range(2))
+    cache.build_tables(plan, lens, new)
+    cache.append(plan, k, v)
+    assert cache.read_status() == 0
+    assert sorted(cache.view("block_table")[[17, 4999], :2].flatten().tolist()) == list(range(pages - 4, pages))
+    q = torch.randn(560, 2 * H, 128, generator=g, device="cuda").half()
+    out = cache.attend(lens, q, plan=plan)
+    for i, (T, row, src) in {17: (300, 299, 0), 4999: (260, 559, 300)}.items():
+        page = cache.view("block_table")[i, 1].item()
+        for h in (0, H - 1):
+            want = _oracle_block(k[src + 128:src + 256, h].cpu().numpy(), v[src + 128:src + 256, h].cpu().numpy(), cache.cfg)
+            for name, w in want.items():
+                assert np.array_equal(_bits(cache.view(name)[page, h].cpu().numpy()), _bits(w)), name
+        table = {i: cache.view("block_table")[i].cpu().numpy()}
+        _check_attention(cache, _Rows(table), [0] * i + [T], q, out, 128 ** -0.5, rows=[None] * i + [row])
+
+
+class _Rows:
+    """Rows of a block table by index, as _rows reads them."""
+
+    def __init__(self, rows):
+        self.rows = rows
+
+    def __getitem__(self, at):
+        return self.rows[at[0]][at[1]]
+
+
 def test_other_stream():
     cache = _cache(num_seqs=2)
     g = torch.Generator("cuda").manual_seed(1)
@@ -625,6 +702,19 @@ def test_other_stream():
     got = cache.attend(lens, q, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+    # a whole step there, of sources that have to be copied first
+    rot = kivi.Rotary()
+    a, b = _cache(num_seqs=2, num_q_heads=4), _cache(num_seqs=2, num_q_heads=4)
+    x = torch.randn(300, 8, 128, generator=g, device="cuda").bfloat16()
+    args = lambda c: (c.new_plan(300), _i32([0, 0]), _i32([170, 130]), x[:, :4], x[:, 4:6], x[:, 6:8])
+    torch.cuda.synchronize()
+    one = a.step(*args(a), rotary=rot, out=torch.zeros(300, 4, 128, dtype=torch.float16, device="cuda"))
+    more = args(b)
+    out = torch.zeros(300, 4, 128, dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    two = b.step(*more, rotary=rot, out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(one, two) and a.read_status() == b.read_status() == 0
 
 
 def test_torch_layer_refusals():
@@ -637,6 +727,11 @@ def test_torch_layer_refusals():
                 lambda: cache.build_tables(plan, lens, lens[:1]), lambda: cache.build_tables(plan, lens, lens, lens_out=lens.long()),
                 lambda: cache.append(plan, q, q[:, :1]), lambda: cache.append(plan, q, q.float()),
                 lambda: cache.step(plan, lens, lens, q.repeat(9, 1, 1), q, q), lambda: cache.new_plan(0)):
+        with pytest.raises(ValueError):
+            bad()
+    other = _cache(num_seqs=3).new_plan(16)  # a plan of another geometry
+    for bad in (lambda: cache.build_tables(other, lens, lens), lambda: cache.append(other, q, q), lambda: cache.attend(lens, q, plan=other),
+                lambda: cache.attend(lens, q, plan=_cache(num_seqs=2, residual=256).new_plan(16))):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(kivi.KiviError):

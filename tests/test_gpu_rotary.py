@@ -134,5 +134,13 @@ def test_step_rotary_of_the_contiguous_cache():
             pos = torch.full((2,), 126 + step, dtype=torch.int32, device="cuda")
             q2, k2, _ = rot.apply(q, kn, positions=pos, q_weight=w, k_weight=w)
             assert torch.equal(out, b.step(k2, vn.half(), q2))
-        assert (a.n_quant, a.n_res) == (b.n_quant, b.n_res) == (128, 3)
+        # slices of a fused projection are the same rows
+        x = torch.randn(2, 8, 128, generator=g, device="cuda").to(dtype)
+        q, kn, vn = x[:, :4], x[:, 4:6], x[:, 6:]
+        out = a.step_rotary(rot, kn, vn, q)
+        assert torch.equal(out, b.step_rotary(rot, kn.contiguous(), vn.contiguous(), q.contiguous()))
+        with pytest.raises(ValueError):
+            a.step_rotary(rot, kn[:, :1], vn, q)
+        assert (a.n_quant, a.n_res) == (b.n_quant, b.n_res) == (128, 4)
+        assert torch.equal(a.view("v_res")[:, :, :4], b.view("v_res")[:, :, :4])
         assert torch.equal(a.view("k_codes")[:, :, :128], b.view("k_codes")[:, :, :128])
