@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libkivi.so")
 LIB_DEBUG = os.path.join(PKG, "libkivi_debug.so")   # -DKIVI_DEBUG: device-side bounds checks
 SOURCES = ["kivi_api.cu", "quantize.cu", "decode.cu", "noalloc.cu", "paged_api.cu", "tables.cu", "rotary.cu", "append.cu",
            "attend.cu"]
-HEADERS = ["common.cuh", "kernels.h", "quant_rules.cuh", "quant_tiles.cuh", "paged.h"]
+HEADERS = ["common.cuh", "kernels.h", "quant_rules.cuh", "quant_tiles.cuh", "overlap.cuh", "paged.h"]
 
 
 def nvcc() -> str:

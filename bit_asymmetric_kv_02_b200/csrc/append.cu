@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "overlap.cuh"
 #include "paged.h"
 #include "quant_rules.cuh"
 #include "quant_tiles.cuh"
@@ -41,6 +42,7 @@ __device__ __forceinline__ bool run_ok(const PagedAppendArgs& a, const Run& r, i
 // block = 2R threads.  A run that completes no block takes a CTA per NT / 16 heads, for K and V both.
 template <int BITS, int NT>
 __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  after_previous_kernel();
   constexpr int P = 32 / BITS, R = NT / 2, kRowHeads = NT / 16;
   int r = static_cast<int>(blockIdx.x / a.heads);
   const int h = static_cast<int>(blockIdx.x % a.heads);
@@ -123,13 +125,9 @@ template <int BITS>
 cudaError_t launch(const PagedAppendArgs& a, cudaStream_t stream) {
   const int runs = a.max_runs < a.max_tokens ? a.max_runs : a.max_tokens;  // a run holds at least one new token
   const dim3 grid(static_cast<unsigned>(runs) * a.heads, 2);
-  if (a.residual == 128)
-    paged_append_kernel<BITS, 256><<<grid, 256, 0, stream>>>(a);
-  else if (a.residual == 256)
-    paged_append_kernel<BITS, 512><<<grid, 512, 0, stream>>>(a);
-  else
-    paged_append_kernel<BITS, 1024><<<grid, 1024, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (a.residual == 128) return launch_overlapped(paged_append_kernel<BITS, 256>, grid, 256, 0, stream, a);
+  if (a.residual == 256) return launch_overlapped(paged_append_kernel<BITS, 512>, grid, 512, 0, stream, a);
+  return launch_overlapped(paged_append_kernel<BITS, 1024>, grid, 1024, 0, stream, a);
 }
 
 }  // namespace

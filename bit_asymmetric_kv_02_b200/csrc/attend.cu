@@ -28,6 +28,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "overlap.cuh"
 #include "paged.h"
 
 namespace kivi {
@@ -1456,6 +1457,7 @@ struct CoreOf<BITS, 0> {
 
 template <int BITS, int NB>
 __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+  after_previous_kernel();
   constexpr int W = attend_warps<NB>(), T = W * 32, UT = CoreOf<BITS, NB>::type::UT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = WarpSmem<BITS, NB>;
@@ -1525,8 +1527,7 @@ cudaError_t launch(const AttendArgs& a, int ctas, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(attend_kernel<BITS, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attend_kernel<BITS, NB><<<ctas, attend_warps<NB>() * 32, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(attend_kernel<BITS, NB>, dim3(ctas), attend_warps<NB>() * 32, smem, stream, a);
 }
 
 struct Shape {

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 #include "paged.h"
 
 namespace kivi {
@@ -63,6 +64,7 @@ template <bool BF16, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads, 3) rotary_kernel(const __grid_constant__ RotaryArgs a, int share) {
   __shared__ __align__(16) float2 cs[kRotaryWarps][kHeadDim / 2];
   __shared__ uint4 ring[kRotaryWarps][kDepth][2][32];  // a lane's two chunks of the head rows on their way
+  after_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned row = blockIdx.x * kRotaryWarps + warp;
   if (row >= static_cast<unsigned>(a.batch) * a.tokens) return;  // below 2^31
@@ -198,18 +200,10 @@ cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t stream) {
   if (share > a.heads) share = a.heads;
   const dim3 grid(static_cast<unsigned>((rows + kRotaryWarps - 1) / kRotaryWarps), static_cast<unsigned>((a.heads + share - 1) / share));
   const int n = static_cast<int>(share);
-  if (dtype == KIVI_DTYPE_BF16) {
-    if (a.interleaved)
-      rotary_kernel<true, true><<<grid, kRotaryThreads, 0, stream>>>(a, n);
-    else
-      rotary_kernel<true, false><<<grid, kRotaryThreads, 0, stream>>>(a, n);
-  } else {
-    if (a.interleaved)
-      rotary_kernel<false, true><<<grid, kRotaryThreads, 0, stream>>>(a, n);
-    else
-      rotary_kernel<false, false><<<grid, kRotaryThreads, 0, stream>>>(a, n);
-  }
-  return cudaGetLastError();
+  const bool bf16 = dtype == KIVI_DTYPE_BF16, side = a.interleaved != 0;
+  auto* kernel = bf16 ? (side ? rotary_kernel<true, true> : rotary_kernel<true, false>)
+                      : (side ? rotary_kernel<false, true> : rotary_kernel<false, false>);
+  return launch_overlapped(kernel, grid, kRotaryThreads, 0, stream, a, n);
 }
 
 }  // namespace kivi

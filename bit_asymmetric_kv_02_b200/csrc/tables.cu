@@ -15,6 +15,7 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 #include "paged.h"
 
 namespace kivi {
@@ -121,6 +122,7 @@ __device__ __forceinline__ long long runs_of(const TablesArgs& a, const RowNeeds
 }
 
 __global__ void __launch_bounds__(kTablesThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
+  after_previous_kernel();
   extern __shared__ int32_t sm[];
   const int n = a.num_rows, tid = threadIdx.x;
   int32_t* cu = sm;               // [n + 1] new tokens
@@ -299,12 +301,14 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(small ? 256 : kTablesThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // overlap.cuh
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, tables_kernel, a);
 }
 
