@@ -47,10 +47,11 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(co
   int r = static_cast<int>(blockIdx.x / a.heads);
   const int h = static_cast<int>(blockIdx.x % a.heads);
   Run run = load_run(a.runs, r);  // r < max_runs: the plan holds that many, used or not
-  const int num_runs = min(__ldg(a.counts), a.max_runs);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (__ldg(a.counts) > a.max_runs || __ldg(a.counts + 1) > a.max_tokens))
-    report_status(a.status, KIVI_ERR_INTERNAL);  // a plan of more than the source or the plan's arrays hold: what fits is done
+  const int2 counts = __ldg(reinterpret_cast<const int2*>(a.counts));  // runs, tokens
+  const int num_runs = min(counts.x, a.max_runs);
   if (r >= num_runs) return;
+  if (r == 0 && (counts.x > a.max_runs || counts.y > a.max_tokens))
+    report_status(a.status, KIVI_ERR_INTERNAL);  // a plan of more than the source or its own arrays hold: what fits is done
   if (run.flags & 2) return;  // done by the run that chains to it
   const int c = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * kTileTokens;
   if (run.page < 0 && run.chain == 0) {
