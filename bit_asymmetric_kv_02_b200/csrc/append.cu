@@ -3,7 +3,10 @@
 // One CTA per (run, KV head, K or V), 2R threads, each holding an 8-token x 8-channel tile of the
 // block in registers (quant_tiles.cuh): a block that the step completes is read once - its first rows
 // from the residual, where earlier steps left them, the others from the new tokens - and its codes and
-// (s, z) come from the same registers.  One pass over the new tokens bounds it.
+// (s, z) come from the same registers.  One pass over the new tokens bounds it: 4 prompts of up to 32768
+// tokens x 32 heads (1.72 GB) take 334 us, 80% of the copy bandwidth.  A step of 64 single tokens x 32 heads,
+// 16 of which complete a block, takes 14 us against 6.5 us for its bytes: three dependent loads and the launch
+// of 4416 blocks, most of which find nothing to do.
 // A sequence's residual holds its newest block, so the run that completes the block the residual still
 // holds part of must read those rows before the sequence's last run overwrites them: the two are
 // chained, done by one CTA in that order.

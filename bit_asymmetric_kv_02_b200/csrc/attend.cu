@@ -25,6 +25,17 @@
 // two from the largest |q|, s of the block and s seen so far, which keep the operands inside fp16.
 // Five to eight queries per KV head take two column blocks over the same A operands; more take passes.
 // The tokens of a K tile are ordered so that a lane's logits are the pairs its P operand needs.
+// One query per KV head takes integer products of bytes instead (struct One).
+//
+// What bounds it.  Read-only streams reach about the copy bandwidth here (6.46 TB/s), 1.25 us for the 8 KB of
+// every SM.  An SM issues an mma m16n8k16 every 2.0 clocks and a logic instruction for four warps every 2, and
+// beside an mma four of the latter take 2.8: with 128 products and 640 masks and shifts per 8 KB at 2 bits, the
+// instructions set the time for 2 to 4 queries (590 clocks per 8 KB, 43% of the copy bandwidth), and at
+// 4 bits, with half of either, nearly so.  One query on bytes (192 masks, 64 products) comes to 78% to 82%.
+//   64 rows of up to 8192 tokens x 32 heads, 2 bits:                170 us (859 MB)
+//   4 rows of up to 32001 tokens x 32 heads, 4 bits:                 95 us (502 MB)
+//   16 rows of up to 32768 tokens x 8 KV heads x 4 queries, 2 bits:  74 us (204 MB)
+// The rest is start and end: about 2 us until the ranges are known, 3.5 us for the first unit, 3 us to join.
 #include <cstdint>
 
 #include "common.cuh"
@@ -45,15 +56,11 @@ constexpr int kMaxCtas = 160;
 constexpr float kNoMax = -1e38f;                  // reference of a part without tokens: finite, and below every other
 constexpr float kSlack = 4.f;                     // logits may pass the reference by this much: weights up to 2^4
 
-#ifndef KIVI_ATTEND_WARPS
-#define KIVI_ATTEND_WARPS 12
-#endif
-#ifndef KIVI_ATTEND_WARPS_ONE
-#define KIVI_ATTEND_WARPS_ONE 16
-#endif
+// Warps per CTA, one CTA per SM: what registers (128, 168 and 255 a thread, next to nothing spilled) and shared memory leave room
+// for.  Fewer are slower: one query 16 warps 166 us, 12 warps 174; four queries 12 warps 74 us, 8 warps 78, 10 warps 82.
 template <int NB>
 __host__ __device__ constexpr int attend_warps() {
-  return NB == 0 ? KIVI_ATTEND_WARPS_ONE : (NB == 1 ? KIVI_ATTEND_WARPS : 8);
+  return NB == 0 ? 16 : (NB == 1 ? 12 : 8);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -1,10 +1,13 @@
 // Norms of queries and keys per head with the position rotation, in one pass, rounded once to the
 // fp16 the cache holds.
 //
-// One memory pass (2 bytes read and written per element) bounds it.  A warp takes a token and its heads, four head rows at a
-// time: 8 lanes hold one head row (two 16-byte chunks each, chosen so that a pair's two channels are in the same lane for every
-// layout), and the rows of the next four steps are on their way to shared memory meanwhile.  The token's cosines and sines are formed once, two pairs a lane,
-// and stay in registers with the norm's weights multiplied in, four factors a pair.
+// One memory pass (2 bytes read and written per element) bounds it.  A warp takes a token and its heads,
+// four head rows at a time: 8 lanes hold one head row (two 16-byte chunks each, chosen so that a pair's two
+// channels are in the same lane for every layout).  The token's cosines and sines are formed once, two pairs
+// a lane, and stay in registers with the norm's weights multiplied in, four factors a pair.  The rows of the
+// next four steps are on their way to shared memory meanwhile: 32768 tokens x 40 heads in bf16 take 111 us,
+// 94% of the copy bandwidth; with one step ahead in registers (24 KB in flight per SM) 141 us, and with
+// blocks of four tokens that read their cosines from shared memory for every head 145 us.
 //
 // The angle is exact: turns[i] is a pair's frequency in turns per position as a 64-bit fraction, so
 // position * turns[i] modulo 2^64 is the fraction of a turn without any rounding (a float32 product

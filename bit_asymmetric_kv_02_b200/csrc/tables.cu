@@ -7,9 +7,10 @@
 // no CTA waits for another's result.  The cluster barrier at the end only orders the last writes
 // (lengths and queue) behind every CTA's reads, so that both may be updated in place.
 //
-// Latency bounds it: the loads of lengths and pages (0.7 us each) and the barriers of the scans.  One scan takes all four sums as
-// if every row could be served; where one cannot, a second one takes those that depend on it.  Small steps take one CTA of eight
-// warps, whose barriers are cheaper.
+// Latency bounds it: the loads of lengths and pages (0.7 us each) and the barriers of the scans.  One scan
+// takes all four sums as if every row could be served; where one cannot, a second one takes those that depend
+// on it.  Small steps take one CTA of eight warps, whose barriers are cheaper.  64 rows of one new token: 5.7 us;
+// 1000 rows of 250 to 500 new tokens: 15 us, half of them the positions (1.5 MB from eight SMs).
 #include <cstdint>
 
 #include <cooperative_groups.h>

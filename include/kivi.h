@@ -363,8 +363,9 @@ int kivi_rotary_apply(const kivi_rotary* rotary, int32_t dtype, int32_t batch, i
  *   head <= i < tail, are free.  The caller starts it with every page (head 0, tail num_pages).
  * Lengths live on the device (int32, one per sequence), so a captured graph of the calls below can be
  * replayed step after step.  Rules: the group, bits and head_dim rules of kivi_config; residual in
- * {128, 256, 512}; 1 <= num_seqs <= 8192; num_pages, max_blocks, num_kv_heads >= 1; max_blocks * R and
- * num_seqs * H * R below 2^31.  Base groups only.
+ * {128, 256, 512}; 1 <= num_seqs <= 8192; num_pages, max_blocks, num_kv_heads >= 1; max_blocks * R,
+ * num_seqs * H * R and num_pages * H below 2^31.  Base groups only.  Caches of a model's layers may have
+ * block_table, free_pages and queue in common: one kivi_paged_build_tables a step serves them all.
  */
 typedef struct kivi_paged_config {
   int32_t num_pages, num_seqs, max_blocks;
@@ -423,14 +424,16 @@ int kivi_paged_build_tables(const kivi_paged_config* cfg, const kivi_paged_cache
  * blocks that the step completes, codes and (s, z) into their page, bit-exactly as kivi_flush_residual
  * would.  k_dev, v_dev: fp16, new token t of head h at t * token_stride + h * head_stride (elements,
  * multiples of 8), tokens packed in the order of cu_tokens.  A run whose sequence, page or rows lie
- * outside the cache or max_tokens is skipped and KIVI_ERR_INTERNAL reported in dev_status.
- * One kernel launch.
+ * outside the cache or max_tokens is skipped and KIVI_ERR_INTERNAL reported in dev_status, as for a plan of
+ * more runs or tokens than max_runs or max_tokens, of which the first are done.  One kernel launch.
  */
 int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
                       const uint16_t* k_dev, const uint16_t* v_dev, int64_t token_stride, int64_t head_stride,
                       int32_t* dev_status, void* stream);
 
-/* Bytes of scratch workspace kivi_paged_decode_attention needs (0 if the arguments are invalid). */
+/* Bytes of scratch workspace kivi_paged_decode_attention needs (0 if the arguments are invalid, or if
+ * num_seqs * H * ceil(Hq / H / 8) heads of max_blocks blocks are more than the kernel's 32-bit counts of 8 KB
+ * units hold: about 2^32 units; KIVI_ERR_UNSUPPORTED from the call). */
 size_t kivi_paged_workspace_bytes(const kivi_paged_config* cfg, int32_t num_q_heads);
 
 /*
@@ -466,7 +469,8 @@ int kivi_abi_version(void);
  * global-memory accesses (copy sources inside the head's arrays and filled tokens, scale indices,
  * destination blocks, residual slots, partial and ticket slots) and, instead of making an access
  * that fails its check, records KIVI_ERR_INTERNAL (in dev_status too, when given) and skips it; no
- * kernel traps.  kivi_debug_status() synchronizes the device and returns the first such status
+ * kernel traps.  (What the paged kernels take from device memory - lengths, pages, runs, query rows - they
+ * check in every build.)  kivi_debug_status() synchronizes the device and returns the first such status
  * since the previous call (KIVI_OK if none), then clears it.  A release build returns
  * KIVI_ERR_UNSUPPORTED.
  */
