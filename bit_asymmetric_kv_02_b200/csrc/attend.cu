@@ -346,24 +346,25 @@ struct Walker {
 
   // ---- units ---------------------------------------------------------------------------------------
   // Runs of plain successors are stepped through in registers; what changes at their ends is in shared memory.
-  __device__ __forceinline__ void fetch() {
-    if (!res) {
-      const uint32_t j = static_cast<uint32_t>(x) >> a.lg_upb;
-      if (table != nullptr) {
-        const int page = __ldg(table + j);  // j < max_blocks: span_of
-        ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
-        blk = static_cast<uint32_t>(ok ? page : 0) * static_cast<uint32_t>(a.heads) + hbase;
-        if (!ok && lane == 0) report_status(a.status, KIVI_ERR_INTERNAL);
-      } else {
-        ok = true;
-        blk = hbase + j;
-      }
-      off = static_cast<long long>(static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHalfBytes << a.lg_upb) +
-                                   (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * kHalfBytes);
+  __device__ __forceinline__ void fetch_codes() {
+    const uint32_t j = static_cast<uint32_t>(x) >> a.lg_upb;
+    if (table != nullptr) {
+      const int page = __ldg(table + j);  // j < max_blocks: span_of
+      ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
+      blk = static_cast<uint32_t>(ok ? page : 0) * static_cast<uint32_t>(a.heads) + hbase;
     } else {
+      ok = true;
+      blk = hbase + j;
+    }
+    off = static_cast<long long>(static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHalfBytes << a.lg_upb) +
+                                 (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * kHalfBytes);
+  }
+  __device__ __forceinline__ void fetch() {
+    if (!res)
+      fetch_codes();
+    else
       off = static_cast<long long>(static_cast<unsigned long long>(blk) * static_cast<uint32_t>((kHeadDim * 2) << a.lg_r) +
                                    static_cast<uint32_t>(x) * kHalfBytes);
-    }
   }
   __device__ __forceinline__ void take(const int4& r) {
     x = r.x;
@@ -391,7 +392,23 @@ struct Walker {
   }
 
   // Copies of a unit's halves, 16 bytes per lane and step; a group is committed whether or not there are any.
+  __device__ __forceinline__ void copy_k_codes() {
+    const uint32_t dst = smem_u32(S.k) + 16 * lane;
+    const char* src = reinterpret_cast<const char*>(a.k_codes) + off + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy16(dst + 512 * i, src + 512 * i);
+  }
+  __device__ __forceinline__ void copy_v_codes() {
+    const uint32_t dst = smem_u32(S.v) + 16 * lane;
+    const char* src = reinterpret_cast<const char*>(a.v_codes) + off + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy16(dst + (i >> 1) * kVPieceStride + (i & 1) * 512, src + 512 * i);
+  }
+  __device__ __forceinline__ void bad_page() const {  // looked at when the copies are due, so that nothing waits for the page before
+    if (lane == 0) report_status(a.status, KIVI_ERR_INTERNAL);
+  }
   __device__ __forceinline__ void issue_k(bool any) {
+    if (any && !ok && !res) bad_page();
     if (any && head) {  // NQ rows of 16 chunks (fewer queries: rows of zeros)
       slot ^= 1;
       const Cursor& c = S.cur;
@@ -405,12 +422,10 @@ struct Walker {
       }
     }
     if (any && ok) {
-      const uint32_t dst = smem_u32(S.k);
       if (!res) {
-        const char* src = reinterpret_cast<const char*>(a.k_codes) + off + 16 * lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) copy16(dst + 16 * lane + 512 * i, src + 512 * i);
+        copy_k_codes();
       } else {
+        const uint32_t dst = smem_u32(S.k);
         const char* src = reinterpret_cast<const char*>(a.k_res) + off + 16 * lane;
 #pragma unroll 1  // a loop, so that the paths stay branches and not sixteen predicated copies
         for (int i = 0; i < 8; ++i) copy16(dst + (lane >> 4) * kRow + (lane & 15) * 16 + 2 * kRow * i, src + 512 * i);
@@ -420,12 +435,10 @@ struct Walker {
   }
   __device__ __forceinline__ void issue_v(bool any) {
     if (any && ok) {
-      const uint32_t dst = smem_u32(S.v);
       if (!res) {
-        const char* src = reinterpret_cast<const char*>(a.v_codes) + off + 16 * lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) copy16(dst + (i >> 1) * kVPieceStride + (i & 1) * 512 + 16 * lane, src + 512 * i);
+        copy_v_codes();
       } else {
+        const uint32_t dst = smem_u32(S.v);
         const char* src = reinterpret_cast<const char*>(a.v_res) + off + 16 * lane;
         const Span& n = S.cur.sp;
         const int tok = n.quant + x * kResTokens + (lane >> 4);
@@ -438,7 +451,9 @@ struct Walker {
   }
   // (s, z) of this lane's piece: K channels 32 t .. 32 t + 31 and V tokens PT t .. PT t + PT - 1
   __device__ __forceinline__ void load_pairs(uint32_t& kp, uint32_t& vp) const {
-    if (!ok || res) return;
+    if (ok && !res) load_code_pairs(kp, vp);
+  }
+  __device__ __forceinline__ void load_code_pairs(uint32_t& kp, uint32_t& vp) const {
     const uint32_t in = (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * UT;
     const size_t ks = static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHeadDim >> a.lg_gk) + ((32 * t) >> a.lg_gk);
     const size_t vs = static_cast<unsigned long long>(blk) * (1u << (a.lg_r - a.lg_gv)) + ((in + PT * t) >> a.lg_gv);
@@ -590,19 +605,40 @@ struct Walker {
         const int ux = x;
         const bool good = ok, more = --left > 0;
         const uint32_t ckp = kp, cvp = vp;
-        if (more) {
+        const bool plain = i + 1 < nq && run_ > 0;  // the next unit is the next one of the same codes: nothing else to look at
+        if (plain) {
+          --run_;
+          ++steps_;
+          ++x;
+          fetch_codes();
+        } else if (more) {
           advance();
           fetch();
         }
         copies_wait<1>();
         if (good) core.quant_k(ux, ckp, cvp);
         __syncwarp();  // the K half has been read, and the P operands are written
-        issue_k(more);
-        if (more) load_pairs(kp, vp);
+        if (plain) {
+          if (ok) {
+            copy_k_codes();
+            load_code_pairs(kp, vp);
+          } else {
+            bad_page();
+          }
+          copies_commit();
+        } else {
+          issue_k(more);
+          if (more) load_pairs(kp, vp);
+        }
         copies_wait<1>();
         if (good) core.quant_v();
         __syncwarp();
-        issue_v(more);
+        if (plain) {
+          if (ok) copy_v_codes();
+          copies_commit();
+        } else {
+          issue_v(more);
+        }
       }
       if (count > nq) {
         typename Core::Res r;
@@ -720,18 +756,21 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   }
 
   // Where a logit (over m) passes the threshold, m moves up to the largest (the first time: to wherever that is), and
-  // o, l and Z with it.  Returns how far.
-  __device__ __forceinline__ float raise(int b, float mu) {
+  // o, l and Z with it.  o also moves to a new V scale exponent (escale).  Returns how far m moved.
+  __device__ __forceinline__ float raise(int b, float mu, float escale) {
     float mx = fmaxf(mu, __shfl_xor_sync(kFull, mu, 4));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-    if (!(mx > thr[b])) return 0.f;
+    if (!(mx > thr[b])) {
+      if (escale != 1.f) scale_o(b, escale);
+      return 0.f;
+    }
     thr[b] = kSlack;
     m[b] += mx;
     const float al = ex2(-fmaxf(mx, 0.f));  // the first time o, l and Z are zero
     l[b] *= al;
     Z[b] *= al;
-    scale_o(b, al);
+    scale_o(b, al * escale);
     return mx;
   }
   __device__ __forceinline__ void scale_o(int b, float f) {
@@ -855,8 +894,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
       eref = max(eref, ev);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float by = raise(b, mu[b]);
-        scale_o(b, escale);
+        const float by = raise(b, mu[b], escale);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           lg[b][i][0] -= by;
@@ -1014,7 +1052,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
     if (__any_sync(kFull, above)) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float by = raise(b, mu[b]), al = ex2(-fmaxf(by, 0.f));
+        const float by = raise(b, mu[b], 1.f), al = ex2(-fmaxf(by, 0.f));
         p[b][0] -= by;
         p[b][1] -= by;
 #pragma unroll
@@ -1145,6 +1183,11 @@ __device__ __forceinline__ void mma_bytes(int (&d)[4], uint32_t a0, uint32_t a1,
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bytes_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -1211,14 +1254,16 @@ struct One : Walker<BITS, 0, One<BITS>> {
     const float fg = static_cast<float>(c[0] * 256 + c[1]) * sc, fh = static_cast<float>(c[2] * 256 + c[3]) * sc;
     return (odd ? fh : fg) + __shfl_xor_sync(kFull, odd ? fg : fh, 1);
   }
-  // Copies of the words of rows g and g + 8 against the operands of one word: W sum c Q of both rows.
+  // Copies of the words of rows g and g + 8 against the operands of one word: W sum c Q of both rows, onto c or (first) alone.
+  template <bool FIRST>
   __device__ static __forceinline__ void products(int (&c)[4], uint32_t wg, uint32_t wh, const uint4& b, int half) {
-    if constexpr (BITS == 2) {
-      mma_bytes(c, wg, wh, wg & 0xFCFCFCFCu, wh & 0xFCFCFCFCu, b.x, b.y);
-      mma_bytes(c, wg & 0xF0F0F0F0u, wh & 0xF0F0F0F0u, wg & 0xC0C0C0C0u, wh & 0xC0C0C0C0u, b.z, b.w);
-    } else {
-      mma_bytes(c, wg, wh, wg & 0xF0F0F0F0u, wh & 0xF0F0F0F0u, half ? b.z : b.x, half ? b.w : b.y);
-    }
+    const uint32_t b0 = BITS == 2 || half == 0 ? b.x : b.z, b1 = BITS == 2 || half == 0 ? b.y : b.w;
+    const uint32_t mask = BITS == 2 ? 0xFCFCFCFCu : 0xF0F0F0F0u;
+    if constexpr (FIRST)
+      mma_bytes_first(c, wg, wh, wg & mask, wh & mask, b0, b1);
+    else
+      mma_bytes(c, wg, wh, wg & mask, wh & mask, b0, b1);
+    if constexpr (BITS == 2) mma_bytes(c, wg & 0xF0F0F0F0u, wh & 0xF0F0F0F0u, wg & 0xC0C0C0C0u, wh & 0xC0C0C0C0u, b.z, b.w);
   }
 
   __device__ __forceinline__ void quant_k(int ux, uint32_t kp, uint32_t vp) {
@@ -1266,7 +1311,7 @@ struct One : Walker<BITS, 0, One<BITS>> {
                                     : S.k + (8 * (g >> 2) + 4 * ((g >> 1) & 1) + (g & 1)) * 64 + 16 * t;
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        int c[4] = {0, 0, 0, 0};
+        int c[4];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint8_t* r0 = kt + 128 * j + 2048 * b;
@@ -1274,14 +1319,20 @@ struct One : Walker<BITS, 0, One<BITS>> {
           const uint4& B1 = b ? bo[1] : be[1];
           if constexpr (BITS == 2) {
             const uint2 wg = *reinterpret_cast<const uint2*>(r0), wh = *reinterpret_cast<const uint2*>(r0 + 1024);
-            products(c, wg.x, wh.x, B0, 0);
-            products(c, wg.y, wh.y, B1, 0);
+            if (b == 0)
+              products<true>(c, wg.x, wh.x, B0, 0);
+            else
+              products<false>(c, wg.x, wh.x, B0, 0);
+            products<false>(c, wg.y, wh.y, B1, 0);
           } else {
             const uint4 wg = *reinterpret_cast<const uint4*>(r0), wh = *reinterpret_cast<const uint4*>(r0 + 1024);
-            products(c, wg.x, wh.x, B0, 0);
-            products(c, wg.y, wh.y, B0, 1);
-            products(c, wg.z, wh.z, B1, 0);
-            products(c, wg.w, wh.w, B1, 1);
+            if (b == 0)
+              products<true>(c, wg.x, wh.x, B0, 0);
+            else
+              products<false>(c, wg.x, wh.x, B0, 0);
+            products<false>(c, wg.y, wh.y, B0, 1);
+            products<false>(c, wg.z, wh.z, B1, 0);
+            products<false>(c, wg.w, wh.w, B1, 1);
           }
         }
         lg[j] = fmaf(gather(c), inv, cst);
@@ -1347,18 +1398,20 @@ struct One : Walker<BITS, 0, One<BITS>> {
     }
     int c[4][4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) c[v][0] = c[v][1] = c[v][2] = c[v][3] = 0;
-#pragma unroll
     for (int x = 0; x < 2; ++x) {
       const uint8_t* row = S.v + t * kVPieceStride + x * 512 + 64 * g;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint4 lo = *reinterpret_cast<const uint4*>(row + 32 * b), hi = *reinterpret_cast<const uint4*>(row + 32 * b + 16);
         const uint4& B = b ? bo[x] : be[x];
-        products(c[0], lo.x, hi.x, B, x);
-        products(c[1], lo.y, hi.y, B, x);
-        products(c[2], lo.z, hi.z, B, x);
-        products(c[3], lo.w, hi.w, B, x);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (x == 0 && b == 0)
+            products<true>(c[v], wl[v], wh[v], B, x);
+          else
+            products<false>(c[v], wl[v], wh[v], B, x);
+        }
       }
     }
 #pragma unroll

@@ -689,6 +689,39 @@ class _Rows:
         return self.rows[at[0]][at[1]]
 
 
+def test_graph_with_copies_between():
+    """Copies and fills between the calls of a captured step: each kernel sees what came before it."""
+    H, n = 2, 3
+    a, b = (_cache(num_seqs=n, num_kv_heads=H, num_q_heads=4) for _ in range(2))
+    lens, plan = _i32([0] * n), a.new_plan(3 * n)
+    lens_b, plan_b = _i32([0] * n), b.new_plan(3 * n)
+    host = torch.randn(3 * n, 8, 128).half().pin_memory()
+    x, out = (torch.zeros(r, h, 128, dtype=torch.float16, device="cuda") for r, h in ((3 * n, 8), (n, 4)))
+    new, kept = _i32([3, 2, 1]), torch.zeros(n, dtype=torch.int32, device="cuda")
+    q = torch.zeros(n, 4, 128, dtype=torch.float16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.build_tables(plan, lens, new)
+        kept.copy_(lens)
+        x.copy_(host, non_blocking=True)
+        a.append(plan, x[:, 4:6], x[:, 6:8])
+        x[:, 4:].zero_()
+        q.copy_(x[:n, :4])
+        out.fill_(9.0)
+        a.attend(kept, q, out=out)
+    for step in range(60):
+        host.copy_(torch.randn(host.shape, generator=torch.Generator().manual_seed(step)).half())
+        graph.replay()
+        torch.cuda.synchronize()
+        y = host.cuda()
+        b.build_tables(plan_b, lens_b, new)
+        b.append(plan_b, y[:, 4:6], y[:, 6:8])
+        want = b.attend(lens_b, y[:n, :4].contiguous())
+        assert torch.equal(out, want) and torch.equal(kept, lens_b), step
+    assert a.read_status() == b.read_status() == 0 and lens.tolist() == [180, 120, 60]
+
+
 def test_other_stream():
     cache = _cache(num_seqs=2)
     g = torch.Generator("cuda").manual_seed(1)
