@@ -5,8 +5,8 @@
 // from the residual, where earlier steps left them, the others from the new tokens - and its codes and
 // (s, z) come from the same registers.  One pass over the new tokens bounds it: 4 prompts of up to 32768
 // tokens x 32 heads (1.72 GB) take 334 us, 80% of the copy bandwidth.  A step of 64 single tokens x 32 heads,
-// 16 of which complete a block, takes 14 us against 6.5 us for its bytes: three dependent loads and the launch
-// of 4416 blocks, most of which find nothing to do.
+// 16 of which complete a block, takes 12.3 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
+// loads that depend on one another.
 // A sequence's residual holds its newest block, so the run that completes the block the residual still
 // holds part of must read those rows before the sequence's last run overwrites them: the two are
 // chained, done by one CTA in that order.
@@ -41,43 +41,33 @@ __device__ __forceinline__ bool run_ok(const PagedAppendArgs& a, const Run& r, i
          r.src >= 0 && r.src <= a.max_tokens - (r.hi - r.lo);
 }
 
-// grid: x = runs (at most) x KV heads, heads fastest (neighbours in the token-major source); y = K, V;
-// block = 2R threads.  A run that completes no block takes a CTA per NT / 16 heads, for K and V both.
-template <int BITS, int NT>
-__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
-  after_previous_kernel();
-  constexpr int P = 32 / BITS, R = NT / 2, kRowHeads = NT / 16;
-  int r = static_cast<int>(blockIdx.x / a.heads);
-  const int h = static_cast<int>(blockIdx.x % a.heads);
-  Run run = load_run(a.runs, r);  // r < max_runs: the plan holds that many, used or not
-  const int2 counts = __ldg(reinterpret_cast<const int2*>(a.counts));  // runs, tokens
-  const int num_runs = min(counts.x, a.max_runs);
-  if (r >= num_runs) return;
-  if (r == 0 && (counts.x > a.max_runs || counts.y > a.max_tokens))
-    report_status(a.status, KIVI_ERR_INTERNAL);  // a plan of more than the source or its own arrays hold: what fits is done
-  if (run.flags & 2) return;  // done by the run that chains to it
-  const int c = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * kTileTokens;
-  if (run.page < 0 && run.chain == 0) {
-    if (blockIdx.y != 0 || h % kRowHeads != 0) return;
-    if (!run_ok(a, run, R)) {
-      report_status(a.status, KIVI_ERR_INTERNAL);
-      return;
-    }
-    const int hh = h + (threadIdx.x >> 4);
-    if (hh >= a.heads || !(run.flags & 1)) return;
-    const long long from = run.src * a.token_stride + hh * a.head_stride;
-    const size_t to = ((static_cast<size_t>(run.seq) * a.heads + hh) * R + run.lo) * kChunks + c;
-    uint4 *kr = reinterpret_cast<uint4*>(a.k_res) + to, *vr = reinterpret_cast<uint4*>(a.v_res) + to;
-#pragma unroll 4
-    for (int i = 0; i < run.hi - run.lo; ++i) {
-      const uint4 k = __ldg(reinterpret_cast<const uint4*>(a.k + from + i * a.token_stride) + c);
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v + from + i * a.token_stride) + c);
-      kr[i * kChunks] = k;
-      vr[i * kChunks] = v;
-    }
+// A run that completes no block: one CTA takes its residual rows of kRowHeads heads from h on, K and V both.
+template <int NT>
+__device__ __forceinline__ void append_rows(const PagedAppendArgs& a, const Run& run, int h) {
+  constexpr int R = NT / 2;
+  if (!run_ok(a, run, R)) {
+    report_status(a.status, KIVI_ERR_INTERNAL);
     return;
   }
-  const bool is_v = blockIdx.y != 0;
+  const int c = threadIdx.x & 15, hh = h + (threadIdx.x >> 4);
+  if (hh >= a.heads || !(run.flags & 1)) return;
+  const long long from = run.src * a.token_stride + hh * a.head_stride;
+  const size_t to = ((static_cast<size_t>(run.seq) * a.heads + hh) * R + run.lo) * kChunks + c;
+  uint4 *kr = reinterpret_cast<uint4*>(a.k_res) + to, *vr = reinterpret_cast<uint4*>(a.v_res) + to;
+#pragma unroll 4
+  for (int i = 0; i < run.hi - run.lo; ++i) {
+    const uint4 k = __ldg(reinterpret_cast<const uint4*>(a.k + from + i * a.token_stride) + c);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v + from + i * a.token_stride) + c);
+    kr[i * kChunks] = k;
+    vr[i * kChunks] = v;
+  }
+}
+
+// A run that completes a block, or the chain of runs that begins with it: one CTA per head and K or V.
+template <int BITS, int NT>
+__device__ __forceinline__ void append_block(const PagedAppendArgs& a, Run run, int r, int num_runs, int h, bool is_v) {
+  constexpr int P = 32 / BITS, R = NT / 2;
+  const int c = threadIdx.x & 15, row0 = (threadIdx.x >> 4) * kTileTokens;
   const uint16_t* src = is_v ? a.v : a.k;
   for (;;) {
     if (!run_ok(a, run, R)) {
@@ -125,13 +115,95 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(co
   }
 }
 
+// Runs of the plan that are looked at.
+__device__ __forceinline__ int runs_of(const PagedAppendArgs& a, const int2& counts, bool reports) {
+  if (reports && (counts.x > a.max_runs || counts.y > a.max_tokens))
+    report_status(a.status, KIVI_ERR_INTERNAL);  // a plan of more than the source or its own arrays hold: what fits is done
+  return min(counts.x, a.max_runs);
+}
+
+// grid: x = runs (at most) x KV heads, heads fastest (neighbours in the token-major source); y = K, V; block = 2R threads.
+template <int BITS, int NT>
+__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  after_previous_kernel();
+  constexpr int kRowHeads = NT / 16;
+  const int r = static_cast<int>(blockIdx.x / a.heads), h = static_cast<int>(blockIdx.x % a.heads);
+  const Run run = load_run(a.runs, r);  // r < max_runs: the plan holds that many, used or not
+  const int num_runs = runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), r == 0);
+  if (r >= num_runs || (run.flags & 2)) return;  // flag 2: done by the run that chains to it
+  if (run.page >= 0 || run.chain != 0)
+    append_block<BITS, NT>(a, run, r, num_runs, h, blockIdx.y != 0);
+  else if (blockIdx.y == 0 && h % kRowHeads == 0)
+    append_rows<NT>(a, run, h);
+}
+
+// The same for at most NT runs few of which complete a block: the grid fills the SMs once, and its CTAs go through the work that
+// there is, which each counts for itself.
+template <int BITS, int NT>
+__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_few_kernel(const __grid_constant__ PagedAppendArgs a) {
+  after_previous_kernel();
+  constexpr int kRowHeads = NT / 16;
+  __shared__ int warp_sum[NT / 32], found[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Run mine{};
+  if (tid < a.max_runs) mine = load_run(a.runs, tid);
+  const int num_runs = min(NT, runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), blockIdx.x == 0));
+  const bool blocks = mine.page >= 0 || mine.chain != 0;
+  int work = 0;
+  if (tid < num_runs && !(mine.flags & 2)) work = blocks ? 2 * a.heads : (a.heads + kRowHeads - 1) / kRowHeads;
+  int before = work;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += y;
+  }
+  if (lane == 31) warp_sum[warp] = before;
+  __syncthreads();
+  before -= work;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    if (i < warp) before += warp_sum[i];
+    total += warp_sum[i];
+  }
+  for (int item = static_cast<int>(blockIdx.x); item < total; item += static_cast<int>(gridDim.x)) {
+    if (item >= before && item < before + work) {
+      found[0] = tid;
+      found[1] = item - before;
+    }
+    __syncthreads();
+    const int r = found[0], i = found[1];
+    const Run run = load_run(a.runs, r);
+    if (run.page >= 0 || run.chain != 0)
+      append_block<BITS, NT>(a, run, r, num_runs, i >> 1, i & 1);
+    else
+      append_rows<NT>(a, run, i * kRowHeads);
+    __syncthreads();
+  }
+}
+
+template <int BITS, int NT>
+cudaError_t launch_tiles(const PagedAppendArgs& a, cudaStream_t stream) {
+  const int runs = a.max_runs < a.max_tokens ? a.max_runs : a.max_tokens;  // a run holds at least one new token
+  const long long ctas = 2ll * runs * a.heads;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  // Few of the runs complete a block when there are few tokens to a run: then most of a grid of all runs x heads finds nothing to
+  // do, and a grid that fills the SMs once takes over, if that one does not.  R = 128, 32 heads, that grid against this one: 64
+  // single tokens 18.4 -> 16.4 us, 64 x up to 60 tokens 34.0 -> 29.2, 16 single tokens 10.2 -> 8.2; but 4 prompts of up to 300 tokens
+  // 16.4 -> 21.2 and of up to 6000 90 -> 125, where blocks that start as others end keep the SMs fuller.
+  const int slots = sms * (kThreadsPerSm / NT);
+  if (runs <= NT && a.max_tokens < runs * (NT / 8) && ctas > slots)
+    return launch_overlapped(paged_append_few_kernel<BITS, NT>, dim3(slots), NT, 0, stream, a);
+  return launch_overlapped(paged_append_kernel<BITS, NT>, dim3(static_cast<unsigned>(runs) * a.heads, 2), NT, 0, stream, a);
+}
 template <int BITS>
 cudaError_t launch(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int runs = a.max_runs < a.max_tokens ? a.max_runs : a.max_tokens;  // a run holds at least one new token
-  const dim3 grid(static_cast<unsigned>(runs) * a.heads, 2);
-  if (a.residual == 128) return launch_overlapped(paged_append_kernel<BITS, 256>, grid, 256, 0, stream, a);
-  if (a.residual == 256) return launch_overlapped(paged_append_kernel<BITS, 512>, grid, 512, 0, stream, a);
-  return launch_overlapped(paged_append_kernel<BITS, 1024>, grid, 1024, 0, stream, a);
+  if (a.residual == 128) return launch_tiles<BITS, 256>(a, stream);
+  if (a.residual == 256) return launch_tiles<BITS, 512>(a, stream);
+  return launch_tiles<BITS, 1024>(a, stream);
 }
 
 }  // namespace
