@@ -41,7 +41,12 @@ __device__ __forceinline__ bool run_ok(const PagedAppendArgs& a, const Run& r, i
          r.src >= 0 && r.src <= a.max_tokens - (r.hi - r.lo);
 }
 
-// A run that completes no block: one CTA takes its residual rows of kRowHeads heads from h on, K and V both.
+// A run that completes no block and has few rows takes a CTA for kRowHeads heads, K and V both; a longer one goes the way of the
+// blocks, a CTA per head and K or V, which has all its rows on the way at once.
+constexpr int kFewRows = 8;
+__device__ __forceinline__ bool few_rows(const Run& r) { return r.page < 0 && r.chain == 0 && r.hi - r.lo <= kFewRows; }
+
+// A run of few rows: one CTA takes its residual rows of kRowHeads heads from h on, K and V both.
 template <int NT>
 __device__ __forceinline__ void append_rows(const PagedAppendArgs& a, const Run& run, int h) {
   constexpr int R = NT / 2;
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(co
   const Run run = load_run(a.runs, r);  // r < max_runs: the plan holds that many, used or not
   const int num_runs = runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), r == 0);
   if (r >= num_runs || (run.flags & 2)) return;  // flag 2: done by the run that chains to it
-  if (run.page >= 0 || run.chain != 0)
+  if (!few_rows(run))
     append_block<BITS, NT>(a, run, r, num_runs, h, blockIdx.y != 0);
   else if (blockIdx.y == 0 && h % kRowHeads == 0)
     append_rows<NT>(a, run, h);
@@ -148,9 +153,8 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_few_kerne
   Run mine{};
   if (tid < a.max_runs) mine = load_run(a.runs, tid);
   const int num_runs = min(NT, runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), blockIdx.x == 0));
-  const bool blocks = mine.page >= 0 || mine.chain != 0;
   int work = 0;
-  if (tid < num_runs && !(mine.flags & 2)) work = blocks ? 2 * a.heads : (a.heads + kRowHeads - 1) / kRowHeads;
+  if (tid < num_runs && !(mine.flags & 2)) work = few_rows(mine) ? (a.heads + kRowHeads - 1) / kRowHeads : 2 * a.heads;
   int before = work;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -174,10 +178,10 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_few_kerne
     __syncthreads();
     const int r = found[0], i = found[1];
     const Run run = load_run(a.runs, r);
-    if (run.page >= 0 || run.chain != 0)
-      append_block<BITS, NT>(a, run, r, num_runs, i >> 1, i & 1);
-    else
+    if (few_rows(run))
       append_rows<NT>(a, run, i * kRowHeads);
+    else
+      append_block<BITS, NT>(a, run, r, num_runs, i >> 1, i & 1);
     __syncthreads();
   }
 }
