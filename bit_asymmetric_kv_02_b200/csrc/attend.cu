@@ -1538,7 +1538,7 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
     if (lane >= off) x += y;
   }
   if (lane == 31) warp_sum[warp] = x;
-  __syncthreads();
+  const int active = __syncthreads_count(mine > 0) * per;  // rows with a query, at most
   int before = x - mine;
   for (int i = 0; i < warp; ++i) before += warp_sum[i];
   cum[tid] = before;
@@ -1548,8 +1548,18 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   Split split;
   split.total = static_cast<uint32_t>(cum[T]) * he_count;  // below 2^32: checked on the host
   if (split.total == 0) return;
-  // few units spread over the SMs
+  // Few units are spread over the SMs, but no further than pays: parts of a head that lie in one CTA join in shared memory, those of
+  // several through tickets and global memory, which the last to arrive reads one after another.  A head of no more units than warps
+  // stays in a CTA, a longer one gets two CTAs' worth of SMs unless that makes it more than 20.  One sequence, 2 bits, calls in a row,
+  // against a unit per CTA: 64 tokens x 1 head 10.1 -> 8.0 us, 1024 x 4 12.5 -> 10.0, 2048 x 1 12.9 -> 11.8, 8192 x 1 19.4 -> 12.3 (with
+  // one CTA's worth 13.3), 32000 x 1 26.6 -> 15.1 (two: 15.6); what loses is 4 sequences of up to 1000 x 8: 12.0 -> 12.4.
   split.per_cta = min(static_cast<uint32_t>(W), (split.total + gridDim.x - 1) / gridDim.x);
+  if (split.per_cta < W) {
+    const uint32_t per_head = (static_cast<uint32_t>(cum[T]) + active - 1) / static_cast<uint32_t>(active);
+    uint32_t parts = per_head <= W ? 1 : (per_head + W / 2 - 1) / (W / 2);
+    if (parts > 20) parts = (per_head + W - 1) / W;
+    split.per_cta = max(split.per_cta, (per_head + parts - 1) / parts);  // at most W
+  }
   split.workers = min(split.total, gridDim.x * split.per_cta);
   split.len = split.total / split.workers;
   split.longer = split.total - split.len * split.workers;
