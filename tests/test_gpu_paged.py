@@ -181,6 +181,47 @@ def test_append(bits, R, gk, gv, H):
         cache.view("free_pages").cpu().numpy()[:cache.view("queue")[0].item()])
 
 
+@pytest.mark.parametrize("bits, R, H, n", [(2, 128, 8, 70), (4, 256, 5, 60), (2, 512, 17, 40), (4, 128, 3, 120)])
+def test_append_many_short_runs(bits, R, H, n):
+    """Steps of few tokens for many sequences, some of which fill a block, some with more rows than others; then a bad run
+    among good ones, and a count of more runs than there are."""
+    rng = np.random.default_rng(bits * R + n)
+    cache = _cache(num_pages=2 * n + 8, num_seqs=n, max_blocks=4, num_kv_heads=H, bits=bits, residual=R)
+    lens = torch.zeros(n, dtype=torch.int32, device="cuda")
+    kv = [(np.zeros((0, H, 128), np.float16),) * 2 for _ in range(n)]
+    first = [int(x) for x in rng.integers(0, 3, n) * R // 2 + rng.integers(-3, 1, n)]
+    steps = [[max(0, x) for x in first], [1] * n, [int(x) for x in rng.integers(0, 3, n)],
+             [int(x) for x in np.where(rng.random(n) < 0.1, rng.integers(8, 20, n), 1)]]
+    plans = [cache.new_plan(max(1, sum(steps[0]))), cache.new_plan(4 * n)]
+    for j, new in enumerate(steps):
+        plan = plans[min(j, 1)]
+        kv_new = rng.standard_normal((max(1, sum(new)), 2, H, 128)).astype(np.float16)
+        dev = torch.from_numpy(kv_new).cuda()
+        cache.build_tables(plan, lens, _i32(new))
+        cache.append(plan, dev[:, 0], dev[:, 1])
+        at = 0
+        for i, a in enumerate(new):
+            kv[i] = tuple(np.concatenate([kv[i][e], kv_new[at:at + a, e]]) for e in (0, 1))
+            at += a
+    _check_cache(cache, lens.tolist(), kv)
+    assert cache.read_status() == 0
+    plan, x = plans[1], torch.randn(4 * n, H, 128, device="cuda").half()
+    runs = [[i, -1, i, 0, 1, 1, 0, 0] for i in range(n)]  # a row each
+    runs[n // 2][0] = n
+    plan.runs[:n] = _i32(runs)
+    for count, want in ((n, 11), (n - 1, 11), (n // 2, 0), (1 << 30, 11)):
+        cache.status.zero_()
+        cache.view("k_res").zero_()
+        plan.runs[n:] = 0  # behind the runs: nothing that could be done
+        plan.counts.copy_(_i32([count, n]))
+        cache.append(plan, x, x)
+        assert cache.read_status() == want, count
+        done = cache.view("k_res")[:, :, 0]
+        for i in range(n):
+            on = i < count and i != n // 2
+            assert torch.equal(done[i], x[i] if on else torch.zeros_like(x[i])), (count, i)
+
+
 def test_append_skips_runs_outside_the_cache():
     """Runs that name sequences, pages or rows outside are left out and reported; the others are done."""
     cache = _cache(num_pages=8, num_seqs=2, max_blocks=4, num_kv_heads=1)
@@ -460,6 +501,24 @@ def test_attention_long_and_wide():
     table = _pages(cache, lens, random.Random(3))
     q = torch.randn(90, 64, 128, generator=g, device="cuda").half()
     _check_attention(cache, table, lens[:12], q, cache.attend(_i32(lens), q), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("bits, G", [(2, 1), (4, 1), (2, 4), (4, 7)])
+@pytest.mark.parametrize("H", [1, 3])
+def test_attention_few_units(bits, G, H):
+    """Few units of one row: heads in one block, in several and in many; among rows without tokens; beside a row of another length."""
+    g = torch.Generator("cuda").manual_seed(H)
+    blocks = 120 if H == 3 else 260
+    cache = _cache(num_pages=blocks + 2, num_seqs=70, max_blocks=blocks, num_kv_heads=H, bits=bits)
+    _fill(cache, g)
+    for T in (1, 16, 17, 128, 129, 400, 1024, 1500, 2049, 4100, 9000, 15000) + ((20000, 33000) if H == 1 else ()):
+        for lens in ([T], [0] * 5 + [T] + [0] * 64, [T, 40]):
+            table = _pages(cache, lens, random.Random(T))
+            q = torch.randn(len(lens), H * G, 128, generator=g, device="cuda").half()
+            out = cache.attend(_i32(lens), q)
+            _check_attention(cache, table, lens, q, out, 128 ** -0.5)
+            assert torch.equal(out, cache.attend(_i32(lens), q)), (T, lens)
+    assert cache.read_status() == 0
 
 
 def test_sequences_that_share_pages():
