@@ -4,8 +4,8 @@
 // block in registers (quant_tiles.cuh): a block that the step completes is read once - its first rows
 // from the residual, where earlier steps left them, the others from the new tokens - and its codes and
 // (s, z) come from the same registers.  One pass over the new tokens bounds it: 4 prompts of up to 32768
-// tokens x 32 heads (1.72 GB) take 337 us, 79% of the copy bandwidth, at 4 bits 60%: the codes keep
-// the logic units busy for most of the time.  A step of 64 single tokens x 32 heads,
+// tokens x 32 heads (1.72 GB) take 303 us, 88% of the copy bandwidth, at 4 bits 63%: its codes
+// take half as many instructions again, and a branch each.  A step of 64 single tokens x 32 heads,
 // 16 of which complete a block, takes 12.3 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
 // loads that depend on one another.
 // A sequence's residual holds its newest block, so the run that completes the block the residual still
@@ -43,8 +43,9 @@ __device__ __forceinline__ bool run_ok(const PagedAppendArgs& a, const Run& r, i
 }
 
 // A run that completes no block and has few rows takes a CTA for kRowHeads heads, K and V both; a longer one goes the way of the
-// blocks, a CTA per head and K or V, which has all its rows on the way at once.
-constexpr int kFewRows = 8;
+// blocks, a CTA per head and K or V, which has all its rows on the way at once.  More than 16 rows: 64 sequences of up to 16 new
+// tokens x 32 heads 14.3 us, 22.5 with 8 here; 6 of up to 40 x 8 heads 8.2, 12.3 with 32 here.
+constexpr int kFewRows = 16;
 __device__ __forceinline__ bool few_rows(const Run& r) { return r.page < 0 && r.chain == 0 && r.hi - r.lo <= kFewRows; }
 
 // A run of few rows: one CTA takes its residual rows of kRowHeads heads from h on, K and V both.

@@ -191,7 +191,7 @@ def test_append_many_short_runs(bits, R, H, n):
     kv = [(np.zeros((0, H, 128), np.float16),) * 2 for _ in range(n)]
     first = [int(x) for x in rng.integers(0, 3, n) * R // 2 + rng.integers(-3, 1, n)]
     steps = [[max(0, x) for x in first], [1] * n, [int(x) for x in rng.integers(0, 3, n)],
-             [int(x) for x in np.where(rng.random(n) < 0.1, rng.integers(8, 20, n), 1)]]
+             [int(x) for x in np.where(rng.random(n) < 0.1, rng.integers(8, 30, n), 1)]]
     plans = [cache.new_plan(max(1, sum(steps[0]))), cache.new_plan(4 * n)]
     for j, new in enumerate(steps):
         plan = plans[min(j, 1)]
