@@ -4,9 +4,9 @@
 // block in registers (quant_tiles.cuh): a block that the step completes is read once - its first rows
 // from the residual, where earlier steps left them, the others from the new tokens - and its codes and
 // (s, z) come from the same registers.  One pass over the new tokens bounds it: 4 prompts of up to 32768
-// tokens x 32 heads (1.72 GB) take 303 us, 88% of the copy bandwidth, at 4 bits 63%: its codes
+// tokens x 32 heads (1.72 GB) take 303 to 328 us by GPU, 81% to 88% of the copy bandwidth, at 4 bits 63%: its codes
 // take half as many instructions again, and a branch each.  A step of 64 single tokens x 32 heads,
-// 16 of which complete a block, takes 12.3 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
+// 16 of which complete a block, takes 12.5 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
 // loads that depend on one another.
 // A sequence's residual holds its newest block, so the run that completes the block the residual still
 // holds part of must read those rows before the sequence's last run overwrites them: the two are

@@ -31,9 +31,9 @@
 // every SM.  An SM issues an mma m16n8k16 every 2.0 clocks and a logic instruction for four warps every 2, and
 // beside an mma four of the latter take 2.8: with 128 products and 640 masks and shifts per 8 KB at 2 bits, the
 // instructions set the time for 2 to 4 queries (570 clocks per 8 KB, 48% of the copy bandwidth), and at
-// 4 bits, with half of either, nearly so.  One query on bytes (192 masks, 64 products) comes to 79% to 83%.
-//   64 rows of up to 8192 tokens x 32 heads, 2 bits:                169 us (859 MB)
-//   4 rows of up to 32001 tokens x 32 heads, 4 bits:                 93 us (502 MB)
+// 4 bits, with half of either, nearly so.  One query on bytes (192 masks, 64 products) comes to 75% to 83%.
+//   64 rows of up to 8192 tokens x 32 heads, 2 bits:                162 to 178 us, by GPU (859 MB)
+//   4 rows of up to 32001 tokens x 32 heads, 4 bits:                 94 us (502 MB)
 //   16 rows of up to 32768 tokens x 8 KV heads x 4 queries, 2 bits:  66 us (204 MB)
 // The rest is start and end: about 2 us until the ranges are known, 3.5 us for the first unit, 1.5 us to join heads in a CTA,
 // 3 us and more across CTAs.

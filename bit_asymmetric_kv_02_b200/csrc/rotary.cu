@@ -6,7 +6,7 @@
 // channels are in the same lane for every layout).  The token's cosines and sines are formed once, two pairs
 // a lane, and stay in registers with the norm's weights multiplied in, four factors a pair.  The rows of the
 // next four steps are on their way to shared memory meanwhile: 32768 tokens x 40 heads in bf16 take 112 to
-// 117 us, 89% to 93% of the copy bandwidth; with one step ahead in registers (24 KB in flight per SM) 141 us, and with
+// 122 us by GPU, 85% to 93% of the copy bandwidth; with one step ahead in registers (24 KB in flight per SM) 141 us, and with
 // blocks of four tokens that read their cosines from shared memory for every head 145 us.
 //
 // The angle is exact: turns[i] is a pair's frequency in turns per position as a 64-bit fraction, so
