@@ -205,8 +205,8 @@ cudaError_t launch_tiles(const PagedAppendArgs& a, cudaStream_t stream) {
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // Few of the runs complete a block when there are few tokens to a run: then most of a grid of all runs x heads finds nothing to
   // do, and a grid that fills the SMs once takes over, if that one does not.  R = 128, 32 heads, that grid against this one: 64
-  // single tokens 18.4 -> 16.4 us, 64 x up to 60 tokens 34.0 -> 29.2, 16 single tokens 10.2 -> 8.2; but 4 prompts of up to 300 tokens
-  // 16.4 -> 21.2 and of up to 6000 90 -> 125, where blocks that start as others end keep the SMs fuller.
+  // single tokens 18.4 -> 16.4 us, 64 x up to 60 tokens 26.7 -> 22.5, 16 single tokens 10.2 -> 8.2; but 4 prompts of up to 300
+  // tokens 10.2 -> 12.3 and of up to 6000 84 -> 100, where blocks that start as others end keep the SMs fuller.
   const int slots = sms * (kThreadsPerSm / NT);
   if (runs <= NT && a.max_tokens < runs * (NT / 8) && ctas > slots)
     return launch_overlapped(paged_append_few_kernel<BITS, NT>, dim3(slots), NT, 0, stream, a);
