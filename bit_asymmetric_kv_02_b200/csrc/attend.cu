@@ -14,9 +14,11 @@
 // of which a warp issues one at a time, cost 200 instructions a unit in loops over the pieces).
 //
 // Products.  Both run on the tensor cores in fp16 with fp32 sums (mma m16n8k16), codes as the A operand:
-// a masked code word IS a pair of fp16 subnormals, (w & 0x0003 << 2 j) = code 4^j 2^-24, exact, so an
-// operand register of two codes costs one AND; the 4^-j goes into the B operand.  Codes at bits 10..15
-// of a half are shifted down first.  The eight B columns hold four queries, each as two columns: the
+// a masked code word IS a pair of fp16 subnormals, code 2^(b - 24) at bit b of its half, exact, so an
+// operand register of two codes costs one AND; what b leaves over goes into the B operand.  Codes at bits 0..3
+// of a half are shifted up by 4 and those at 10..15 down by 6 first (2 bits): products of the smallest subnormals lose their
+// last bits in the tensor cores' sums (16 x 8 x 4 queries up to 32768 tokens: error before the rounding 5.0e-5 of the output
+// with codes at bits 0..9, 6.6e-6 with 4..9, in the same time).  The eight B columns hold four queries, each as two columns: the
 // value rounded to fp16 and the rest, so operands carry 22 bits and nothing is lost to fp16:
 //   K: B = q_c s_g(c) 2^x (s changes with every block: one multiply and one fused multiply-add a pair);
 //      the constant sum_g z_g sum_c q_c is added in fp32.
@@ -131,23 +133,23 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t w) { return __half22float2(
 __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// The codes of a word as pairs (j, j + P / 2) of fp16 subnormals: code 4^e(j) 2^-24 (16^e at 4 bits).
-// The upper pairs are taken from the word shifted down (upper_codes).
+// The codes of a word as pairs (j, j + P / 2) of fp16 subnormals: code 2^(kPairLow + pair_shift(j) - 24).  At 2 bits
+// pairs 0 and 1 come from the word shifted up by 4 (by the multiplier, whose pipe is free), 2..4 from the word itself and
+// 5..7 from the word shifted down by 6.
 template <int BITS>
-__device__ __forceinline__ uint32_t upper_codes(uint32_t w) {
-  return w >> (BITS == 2 ? 10 : 8);
-}
-template <int BITS>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t upper, int j) {
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
   if constexpr (BITS == 2)
-    return j < 5 ? w & (0x00030003u << (2 * j)) : upper & (0x00030003u << (2 * (j - 5)));
+    return j < 2 ? (w * 16u) & (0x00300030u << (2 * j))
+                 : (j < 5 ? w & (0x00300030u << (2 * (j - 2))) : (w >> 6) & (0x00300030u << (2 * (j - 5))));
   else
-    return (j < 2 ? w : upper) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
+    return (j < 2 ? w : w >> 8) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
-// log2 of the factor code_pair leaves on pair j.
+template <int BITS>
+constexpr int kPairLow = BITS == 2 ? 4 : 0;
+// log2 of the factor code_pair leaves on pair j, past 2^kPairLow.
 template <int BITS>
 __device__ __forceinline__ constexpr int pair_shift(int j) {
-  return BITS == 2 ? 2 * (j < 5 ? j : j - 5) : 4 * (j & 1);
+  return BITS == 2 ? 2 * (j < 2 ? j : (j < 5 ? j - 2 : j - 5)) : 4 * (j & 1);
 }
 
 // What a sequence of T tokens shows its newest token: t < sink_end or start <= t < T; tokens
@@ -688,9 +690,10 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   static constexpr int HP = P / 2;                  // code pairs per word
   static constexpr int MT = UT / 16;                // K tiles per unit
   static constexpr int KW = kHeadDim / P / 4;       // K words per lane and token
-  // At 4 bits the V codes are all put at bits 4..7 of their halves (code 2^-20): products of the smallest subnormals lose their
-  // last bits, which shows where sum_t p_t z takes most of the sum back (0.00025 -> 0.00021 of the output at 8000 tokens).
-  static constexpr int kVUp = BITS == 4 ? 4 : 0;
+  // V codes are at bit 4 or above of their halves (code 2^-20): the lost bits of lower ones (top of the file) show most where
+  // sum_t p_t z takes most of the sum back.  At 2 bits code_pair has them there; at 4 bits quant_v puts all at bits 4..7.  K codes at
+  // 4 bits stay at bits 0..7: lifting them costs 4% (88 -> 92 us) for an error of 1.4e-5 instead of 1.7e-5, beside a rounding of 2.1e-4.
+  static constexpr int kVUp = 4;
   struct Res {
     float p[NB][2], r[NB][8][4];
   };
@@ -816,14 +819,14 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         for (int j = 0; j < 4; ++j)
           kb[b][4 * i + j] = as_u32(__hfma2(as_h2(w[j]), sh, __hmul2(as_h2(w[j]), nsh)));  // even columns: q s rounded; odd: the rest
       }
-      inv[b] = a.qscale * pow2i(qe[b] + ek - 4);
+      inv[b] = a.qscale * pow2i(qe[b] + ek - 4 - kPairLow<BITS>);
       cst[b] = fmaf(z[3], qs[b][3], fmaf(z[2], qs[b][2], fmaf(z[1], qs[b][1], z[0] * qs[b][0]))) - m[b];
     }
     const uint8_t* kt = S.k + ((g >> 2) * (UT / 2) + jl) * (16 * BITS) + 4 * KW * t;
     // two tiles at a time: two independent chains of sums per column block
 #pragma unroll
     for (int i0 = 0; i0 < MT; i0 += 2) {
-      uint32_t w[2][2][KW], up[2][2][KW];  // [tile][row g, g + 8][word]
+      uint32_t w[2][2][KW];  // [tile][row g, g + 8][word]
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int n = i0 + i;
@@ -843,15 +846,11 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
 #pragma unroll
       for (int x = 0; x < KW; ++x) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) up[i][y][x] = upper_codes<BITS>(w[i][y][x]);
-#pragma unroll
         for (int j = 0; j < HP; j += 2)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t a0 = code_pair<BITS>(w[i][0][x], up[i][0][x], j), a1 = code_pair<BITS>(w[i][1][x], up[i][1][x], j);
-            const uint32_t a2 = code_pair<BITS>(w[i][0][x], up[i][0][x], j + 1), a3 = code_pair<BITS>(w[i][1][x], up[i][1][x], j + 1);
+            const uint32_t a0 = code_pair<BITS>(w[i][0][x], j), a1 = code_pair<BITS>(w[i][1][x], j);
+            const uint32_t a2 = code_pair<BITS>(w[i][0][x], j + 1), a3 = code_pair<BITS>(w[i][1][x], j + 1);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (x == 0 && j == 0)
@@ -911,8 +910,8 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
     for (int tb = 0; tb < 2; ++tb) {
       const float s = h2f(static_cast<uint16_t>(vq[tb])) * kscale;
       if constexpr (BITS == 2) {
-        fac[tb][0] = s * pow2i(-2 * jl);
-        fac[tb][1] = s * (jl == 0 ? 0x1p-8f : pow2i(2 - 2 * jl));
+        fac[tb][0] = s * pow2i(-pair_shift<2>(jl));
+        fac[tb][1] = s * pow2i(-pair_shift<2>(jl + 4));
       } else {
         fac[tb][0] = s;
       }
@@ -992,9 +991,9 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const uint32_t v0 = w[x][e], v1 = w[x][e + 1], u0 = upper_codes<2>(v0), u1 = upper_codes<2>(v1);
-              product(jl == 0 && x == 0, e, code_pair<2>(v0, u0, jl), code_pair<2>(v1, u1, jl), code_pair<2>(v0, u0, jl + 4),
-                      code_pair<2>(v1, u1, jl + 4), jl, x);
+              const uint32_t v0 = w[x][e], v1 = w[x][e + 1];
+              product(jl == 0 && x == 0, e, code_pair<2>(v0, jl), code_pair<2>(v1, jl), code_pair<2>(v0, jl + 4), code_pair<2>(v1, jl + 4),
+                      jl, x);
             }
         } else {
           auto pair = [&](uint32_t v) { return (jl == 0 ? v * 16u : (jl == 1 ? v : v >> (jl == 2 ? 4 : 8))) & 0x00F000F0u; };
