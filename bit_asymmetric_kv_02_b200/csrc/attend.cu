@@ -24,7 +24,8 @@
 //      the constant sum_g z_g sum_c q_c is added in fp32.
 //   V: B = p_t s_g(t) 2^y; sum_t p_t z_g(t) is one scalar per query.
 // The column pair of a query sits in one lane, whose two sums are added there.  x and y are powers of
-// two from the largest |q|, s of the block and s seen so far, which keep the operands inside fp16.
+// two, x from the largest |q| and s of the block, y from the largest p_t s_g(t) of the unit, for each query: the operands stay
+// inside fp16, and a group of large values that has no weight takes no bits from those that have.
 // Five to eight queries per KV head take two column blocks over the same A operands; more take passes.
 // The tokens of a K tile are ordered so that a lane's logits are the pairs its P operand needs.
 // One query per KV head takes integer products of bytes instead (struct One).
@@ -703,7 +704,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   float m[NB], thr[NB], l[NB], Z[NB], o[NB][8][4];
   float qs[NB][4];   // scale * log2 e * sum of q over channels 32 i .. 32 i + 31
   int qe[NB];        // exponent of the largest |q|
-  int eref;          // exponent field of the largest V scale so far: o carries 2^(kVUp - eref) (P operands 2^(24 - eref))
+  float vf[NB];      // of the unit in hand: what its sums of P operands and V codes are times, to join o
 
   using Base::Base;
 
@@ -755,33 +756,30 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[b][v8][i] = 0.f;
     }
-    eref = 1;
     __syncwarp();
   }
 
+  // The largest of a query's lanes.
+  __device__ __forceinline__ static float max_of_query(float x) {
+    x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+    return fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+  }
   // Where a logit (over m) passes the threshold, m moves up to the largest (the first time: to wherever that is), and
-  // o, l and Z with it.  o also moves to a new V scale exponent (escale).  Returns how far m moved.
-  __device__ __forceinline__ float raise(int b, float mu, float escale) {
-    float mx = fmaxf(mu, __shfl_xor_sync(kFull, mu, 4));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-    if (!(mx > thr[b])) {
-      if (escale != 1.f) scale_o(b, escale);
-      return 0.f;
-    }
+  // o, l and Z with it.  Returns how far m moved.
+  __device__ __forceinline__ float raise(int b, float mu) {
+    const float mx = max_of_query(mu);
+    if (!(mx > thr[b])) return 0.f;
     thr[b] = kSlack;
     m[b] += mx;
     const float al = ex2(-fmaxf(mx, 0.f));  // the first time o, l and Z are zero
     l[b] *= al;
     Z[b] *= al;
-    scale_o(b, al * escale);
-    return mx;
-  }
-  __device__ __forceinline__ void scale_o(int b, float f) {
 #pragma unroll
     for (int v8 = 0; v8 < 8; ++v8)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[b][v8][i] *= f;
+      for (int i = 0; i < 4; ++i) o[b][v8][i] *= al;
+    return mx;
   }
 
   // Slot of P operand vector (column n, code pair jl of word rows of lane tt): conflict-free for the
@@ -800,8 +798,8 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
       const int p0 = tok0 + PT * t;
       if (p0 >= S.now.sp.sink_end && p0 + PT <= S.now.sp.start) vp = 0;
     }
-    const unsigned ksm = __reduce_max_sync(kFull, kp & 0xFFFFu), vsm = __reduce_max_sync(kFull, vp & 0xFFFFu);
-    const int ek = max(1, static_cast<int>(ksm >> 10)), ev = max(1, static_cast<int>(vsm >> 10));
+    const unsigned ksm = __reduce_max_sync(kFull, kp & 0xFFFFu);
+    const int ek = max(1, static_cast<int>(ksm >> 10));
     const __half2 sh = __float2half2_rn(h2f(static_cast<uint16_t>(kp)) * pow2i(22 - ek));
     const __half2 nsh = (g & 1) ? __hneg2(sh) : __float2half2_rn(0.f);
     float z[4];
@@ -880,21 +878,25 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
             for (int b = 0; b < NB; ++b) lg[b][i][y] = -INFINITY;
       }
     }
-    float mu[NB];
-    bool above = ev > eref;
+    constexpr int HALF = MT / 2;  // tiles of one tb
+    float mu[NB][2];
+    bool above = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      mu[b] = lg[b][0][0];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) mu[b] = fmaxf(mu[b], fmaxf(lg[b][i][0], lg[b][i][1]));
-      above = above || mu[b] > thr[b];
+      for (int tb = 0; tb < 2; ++tb) {
+        mu[b][tb] = fmaxf(lg[b][tb * HALF][0], lg[b][tb * HALF][1]);
+#pragma unroll
+        for (int i = 1; i < HALF; ++i) mu[b][tb] = fmaxf(mu[b][tb], fmaxf(lg[b][tb * HALF + i][0], lg[b][tb * HALF + i][1]));
+      }
+      above = above || fmaxf(mu[b][0], mu[b][1]) > thr[b];
     }
     if (__any_sync(kFull, above)) {
-      const float escale = pow2i(min(0, eref - ev));
-      eref = max(eref, ev);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float by = raise(b, mu[b], escale);
+        const float by = raise(b, fmaxf(mu[b][0], mu[b][1]));
+        mu[b][0] -= by;
+        mu[b][1] -= by;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           lg[b][i][0] -= by;
@@ -902,23 +904,27 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
         }
       }
     }
-    const float kscale = pow2i(24 - eref);
-    uint32_t vq[2] = {__shfl_sync(kFull, vp, tt0), __shfl_sync(kFull, vp, tt0 + 1)};
+    const uint32_t vq[2] = {__shfl_sync(kFull, vp, tt0), __shfl_sync(kFull, vp, tt0 + 1)};
+    const float vs[2] = {h2f(static_cast<uint16_t>(vq[0])), h2f(static_cast<uint16_t>(vq[1]))};
     constexpr int JJ = BITS == 2 ? 2 : 1;
-    float fac[2][JJ];
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      const float s = h2f(static_cast<uint16_t>(vq[tb])) * kscale;
-      if constexpr (BITS == 2) {
-        fac[tb][0] = s * pow2i(-pair_shift<2>(jl));
-        fac[tb][1] = s * pow2i(-pair_shift<2>(jl + 4));
-      } else {
-        fac[tb][0] = s;
-      }
-    }
-    constexpr int HALF = MT / 2;  // tiles of one tb
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      // operands from 2^14 to 2^15 for the largest p s; 2^-80 and less (weights are up to 2^kSlack) count as nothing
+      const float top = max_of_query(fmaxf(ex2(mu[b][0]) * vs[0], ex2(mu[b][1]) * vs[1]));
+      const int e = min(max(__float_as_int(top) >> 23, 127 - 80), 127 + 121);
+      const float up = pow2i(14 + 127 - e);
+      vf[b] = pow2i(e - 127 - 14 + 24 - kVUp);
+      float fac[2][JJ];
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb) {
+        const float s = vs[tb] * up;
+        if constexpr (BITS == 2) {
+          fac[tb][0] = s * pow2i(-pair_shift<2>(jl));
+          fac[tb][1] = s * pow2i(-pair_shift<2>(jl + 4));
+        } else {
+          fac[tb][0] = s;
+        }
+      }
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb) {
         uint32_t hi[HALF], lo[HALF];
@@ -1007,7 +1013,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[b][2 * i + e][q] += c[e][b][q];
+          for (int q = 0; q < 4; ++q) o[b][2 * i + e][q] = fmaf(c[e][b][q], vf[b], o[b][2 * i + e][q]);
     }
   }
 
@@ -1052,7 +1058,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
     if (__any_sync(kFull, above)) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float by = raise(b, mu[b], 1.f), al = ex2(-fmaxf(by, 0.f));
+        const float by = raise(b, mu[b]), al = ex2(-fmaxf(by, 0.f));
         p[b][0] -= by;
         p[b][1] -= by;
 #pragma unroll
@@ -1100,7 +1106,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   __device__ __forceinline__ void res_end(Res& s) {
     const float(&r)[NB][8][4] = s.r;
     float* buf = reinterpret_cast<float*>(S.p[0]);  // 4 queries at a time of 64 channels: 1 KB
-    const float f = pow2i(kVUp - 10 - eref);
+    constexpr float f = 1.f / 1024.f;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -1130,7 +1136,6 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
   // Lane (g, t): o of query t (each column block), channels 16 g .. 16 g + 15.
   __device__ __forceinline__ void finish(float* part) {
     const int nq = S.now.queries;
-    const float back = pow2i(eref - kVUp);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float ls = l[b], zs = Z[b];
@@ -1144,8 +1149,8 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
       float f[16];
 #pragma unroll
       for (int v8 = 0; v8 < 8; ++v8) {
-        f[2 * v8] = (o[b][v8][0] + o[b][v8][1]) * back;
-        f[2 * v8 + 1] = (o[b][v8][2] + o[b][v8][3]) * back;
+        f[2 * v8] = o[b][v8][0] + o[b][v8][1];
+        f[2 * v8 + 1] = o[b][v8][2] + o[b][v8][3];
       }
       if (part == nullptr) {
         const float inv = ls == 0.f ? 0.f : 1.f / ls;
@@ -1172,7 +1177,7 @@ struct Many : Walker<BITS, NB, Many<BITS, NB>> {
 // A operand of mma m16n8k32 (u8 x s8, int32 sums) takes a code word as it is and its copies without the lowest codes of each
 // byte: V_k = sum over i >= k of c_i 2^(b i), k = 0 .. P / 4 - 1, one AND per copy but the first.  Against
 // X_k = W (Q_k 2^(-b k) - Q_(k-1) 2^(-b (k-1))), W = 2^(b (P / 4 - 1)), the products add up to W sum c_k Q_k, exactly.  Q is
-// q_c s_g(c), P is p_t s_g(t), as fixed point relative to the largest of the block (23 bits) or to its bound (24 bits); each X
+// q_c s_g(c), P is p_t s_g(t), as fixed point relative to the largest of the block (23 bits) or of the unit (24 bits); each X
 // (below 2^30) is four signed byte digits, one B column each.  Two tiles of 16 tokens (or channels) share a sum: the digits of
 // the one sit in columns 0..3, of the other in columns 4..7, each against zeros for the other tile.
 constexpr float kQFixed = 8388544.f;   // 2^23 - 64
@@ -1345,19 +1350,18 @@ struct One : Walker<BITS, 0, One<BITS>> {
       for (int j = 0; j < TJ; ++j)
         if (!seen(S.now.sp, tok0 + P * r + in + NV * j)) lg[j] = -INFINITY;
     }
-    // softmax, and P operands relative to the unit's largest weight times its largest s
+    // softmax, and P operands relative to the unit's largest p s (2^-100 and less count as nothing)
     float mu = lg[0];
 #pragma unroll
     for (int j = 1; j < TJ; ++j) mu = fmaxf(mu, lg[j]);
-    mu = max_of_warp(mu);
-    const float smax = max_of_warp(h2f(static_cast<uint16_t>(vp)));
     const uint32_t vq = __shfl_sync(kFull, vp, r >> 1);
-    const float mn = fmaxf(m, mu), d = mu - mn;  // d <= 0: the unit's largest weight is 2^d
+    const float vs = h2f(static_cast<uint16_t>(vq)), mn = fmaxf(m, max_of_warp(mu));
     alpha = ex2(m - mn);
     m = mn;
-    const bool some = d > -64.f && smax > 0.f;
-    const float f = some ? kPFixed * reciprocal(smax) * ex2(-d) * h2f(static_cast<uint16_t>(vq)) : 0.f;
-    invv = some ? ex2(d) * smax * (1.0f / (W * kPFixed)) : 0.f;
+    const float top = max_of_warp(ex2(mu - mn) * vs);
+    const bool some = top > 0x1p-100f;
+    const float f = some ? kPFixed * reciprocal(top) * vs : 0.f;
+    invv = some ? top * (1.0f / (W * kPFixed)) : 0.f;
     const int xa = W >> (BITS * k), xb = k ? (W << BITS) >> (BITS * k) : 0;
     float ps = 0.f;
     int xs[4] = {0, 0, 0, 0};
