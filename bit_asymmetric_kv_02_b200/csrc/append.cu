@@ -28,7 +28,7 @@ struct Run {
 
 __device__ __forceinline__ Run load_run(const int32_t* runs, int r) {
   const int4* p = reinterpret_cast<const int4*>(runs) + 2 * static_cast<size_t>(r);
-  const int4 a = __ldg(p), b = __ldg(p + 1);
+  const int4 a = p[0], b = p[1];
   return {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
 }
 
@@ -61,12 +61,22 @@ __device__ __forceinline__ void append_rows(const PagedAppendArgs& a, const Run&
   const long long from = run.src * a.token_stride + hh * a.head_stride;
   const size_t to = ((static_cast<size_t>(run.seq) * a.heads + hh) * R + run.lo) * kChunks + c;
   uint4 *kr = reinterpret_cast<uint4*>(a.k_res) + to, *vr = reinterpret_cast<uint4*>(a.v_res) + to;
-#pragma unroll 4
-  for (int i = 0; i < run.hi - run.lo; ++i) {
-    const uint4 k = __ldg(reinterpret_cast<const uint4*>(a.k + from + i * a.token_stride) + c);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v + from + i * a.token_stride) + c);
-    kr[i * kChunks] = k;
-    vr[i * kChunks] = v;
+  const int rows = run.hi - run.lo;
+#pragma unroll 1
+  for (int i0 = 0; i0 < rows; i0 += 4) {  // four rows on their way at once
+    uint4 k[4], v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= rows) break;
+      k[i] = *(reinterpret_cast<const uint4*>(a.k + from + (i0 + i) * a.token_stride) + c);
+      v[i] = *(reinterpret_cast<const uint4*>(a.v + from + (i0 + i) * a.token_stride) + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= rows) break;
+      kr[(i0 + i) * kChunks] = k[i];
+      vr[(i0 + i) * kChunks] = v[i];
+    }
   }
 }
 
@@ -143,7 +153,7 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_kernel(co
   constexpr int kRowHeads = NT / 16;
   const int r = static_cast<int>(blockIdx.x / a.heads), h = static_cast<int>(blockIdx.x % a.heads);
   const Run run = load_run(a.runs, r);  // r < max_runs: the plan holds that many, used or not
-  const int num_runs = runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), r == 0);
+  const int num_runs = runs_of(a, *reinterpret_cast<const int2*>(a.counts), r == 0);
   if (r >= num_runs || (run.flags & 2)) return;  // flag 2: done by the run that chains to it
   if (!few_rows(run))
     append_block<BITS, NT, true>(a, run, r, num_runs, h, blockIdx.y != 0);
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_few_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Run mine{};
   if (tid < a.max_runs) mine = load_run(a.runs, tid);
-  const int num_runs = min(NT, runs_of(a, __ldg(reinterpret_cast<const int2*>(a.counts)), blockIdx.x == 0));
+  const int num_runs = min(NT, runs_of(a, *reinterpret_cast<const int2*>(a.counts), blockIdx.x == 0));
   int work = 0;
   if (tid < num_runs && !(mine.flags & 2)) work = few_rows(mine) ? (a.heads + kRowHeads - 1) / kRowHeads : 2 * a.heads;
   int before = work;

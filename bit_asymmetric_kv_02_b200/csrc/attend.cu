@@ -163,7 +163,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b, bool* bad) {
   Span s;
   *bad = false;
   if (a.lens != nullptr) {
-    s.len = __ldg(a.lens + b);
+    s.len = a.lens[b];
     if (s.len < 0 || (s.len > 0 && ((s.len - 1) >> a.lg_r) > a.max_blocks)) {
       *bad = true;
       s.len = 0;
@@ -203,8 +203,8 @@ __device__ __forceinline__ Units units_of(const Span& s) {
 __device__ __forceinline__ int q_row(const AttendArgs& a, int b, bool* bad) {
   int row = b;
   if (a.cu_tokens != nullptr) {
-    const int next = __ldg(a.cu_tokens + b + 1);
-    if (next == __ldg(a.cu_tokens + b)) return -1;
+    const int next = a.cu_tokens[b + 1];
+    if (next == a.cu_tokens[b]) return -1;
     row = next - 1;
   }
   if (row < 0 || row >= a.q_rows) {
@@ -353,7 +353,7 @@ struct Walker {
   __device__ __forceinline__ void fetch_codes() {
     const uint32_t j = static_cast<uint32_t>(x) >> a.lg_upb;
     if (table != nullptr) {
-      const int page = __ldg(table + j);  // j < max_blocks: span_of
+      const int page = table[j];  // j < max_blocks: span_of
       ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages);
       blk = static_cast<uint32_t>(ok ? page : 0) * static_cast<uint32_t>(a.heads) + hbase;
     } else {
@@ -461,8 +461,8 @@ struct Walker {
     const uint32_t in = (static_cast<uint32_t>(x) & ((1u << a.lg_upb) - 1)) * UT;
     const size_t ks = static_cast<unsigned long long>(blk) * static_cast<uint32_t>(kHeadDim >> a.lg_gk) + ((32 * t) >> a.lg_gk);
     const size_t vs = static_cast<unsigned long long>(blk) * (1u << (a.lg_r - a.lg_gv)) + ((in + PT * t) >> a.lg_gv);
-    kp = static_cast<uint32_t>(__ldg(a.k_scale + ks)) | (static_cast<uint32_t>(__ldg(a.k_zero + ks)) << 16);
-    vp = static_cast<uint32_t>(__ldg(a.v_scale + vs)) | (static_cast<uint32_t>(__ldg(a.v_zero + vs)) << 16);
+    kp = static_cast<uint32_t>(a.k_scale[ks]) | (static_cast<uint32_t>(a.k_zero[ks]) << 16);
+    vp = static_cast<uint32_t>(a.v_scale[vs]) | (static_cast<uint32_t>(a.v_zero[vs]) << 16);
   }
   __device__ static __forceinline__ bool seen(const Span& n, int tok) {
     return tok < n.len && (tok < n.sink_end || tok >= n.start);

@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kRotaryThreads, 3) rotary_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
       if (w != nullptr) {
-        unpack8<BF16>(__ldg(w + ca), wa);
-        unpack8<BF16>(__ldg(w + cb), wb);
+        unpack8<BF16>(w[ca], wa);
+        unpack8<BF16>(w[cb], wb);
       }
       const float4* c4 = reinterpret_cast<const float4*>(cs[warp]) + j;
 #pragma unroll
