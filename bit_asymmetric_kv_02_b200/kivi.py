@@ -470,6 +470,12 @@ def _vector(owner, name: str, t, n, dtype) -> None:
         _expect(owner, name, t, (n,), dtype)
 
 
+def _row_strides(t) -> tuple:
+    """Strides of a [tokens][heads][128] tensor's first two dimensions; 0 where the extent leaves them without meaning."""
+    (n, h, _), (a, b, _) = t.shape, t.stride()
+    return a if n > 1 else 0, b if h > 1 else 0
+
+
 def _raw_stream(owner, stream) -> int:
     """The handle of `stream`, or of the owner's device's current stream."""
     return stream.cuda_stream if stream is not None else owner.torch._C._cuda_getCurrentRawStream(owner.index)
@@ -748,11 +754,11 @@ class PagedKiviCache:
         shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
         _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
         _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
-        sk = k.stride()
-        if sk[2] != 1 or sk != v.stride():
-            raise ValueError(f"k, v: strides {sk} and {v.stride()}; want equal strides and contiguous channels")
         if k.shape[0] == 0:
             return
+        sk = _row_strides(k)
+        if sk != _row_strides(v) or k.stride(2) != 1 or v.stride(2) != 1:
+            raise ValueError(f"k, v: strides {k.stride()} and {v.stride()}; want equal strides and contiguous channels")
         c = plan.c
         if k.shape[0] < plan.max_tokens:  # a plan of more tokens than there are rows must not read past them
             c = kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, k.shape[0], c.max_runs)
@@ -796,9 +802,9 @@ class PagedKiviCache:
                                      positions=plan.positions[:q.shape[0]], q_weight=q_weight, k_weight=k_weight, eps=eps,
                                      stream=stream)
             v = v if v16 is None else v16
-        if k.stride() != v.stride() or not q.is_contiguous():
+        if _row_strides(k) != _row_strides(v) or not q.is_contiguous():
             with self.torch.cuda.stream(stream):  # None: the current stream
-                if k.stride() != v.stride():
+                if _row_strides(k) != _row_strides(v):
                     k, v = k.contiguous(), v.contiguous()
                 q = q.contiguous()
         self.append(plan, k, v, stream=stream, status=status)
