@@ -590,6 +590,12 @@ class Rotary:
         [B][heads][T][128], of any strides that keep head rows whole (slices of a fused projection).
         positions: int32 device tensor of one entry per token ([tokens] or [B][T]), or the first position.
         Outputs may be given; an fp16 input may be its own output."""
+        call, outputs = self._arguments(q, k, v, positions, q_weight, k_weight, eps, q_out, k_out, v_out, stream)
+        self._launch(call)
+        return outputs
+
+    def _arguments(self, q, k, v, positions, q_weight, k_weight, eps, q_out, k_out, v_out, stream) -> tuple:
+        """apply()'s checks: what _launch takes, and the outputs."""
         torch = self.torch
         dtype = DTYPE_F16 if q.dtype is torch.float16 else DTYPE_BF16
         n = q.dim()
@@ -609,18 +615,24 @@ class Rotary:
                     or positions.device != q.device:
                 raise ValueError(f"positions: want contiguous int32 of {batch * tokens} entries on {q.device}")
             ptr, first = positions.data_ptr(), 0
-        if batch * tokens == 0:
-            return q_out, k_out, v_out
         index = q.get_device()
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-        call = load_library().kivi_rotary_apply
-        if index == torch._C._cuda_getDevice():
-            st = call(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
+        return (index, batch, tokens, (self.c, dtype), (ptr, first, hq, hk, hv, eps, s)), (q_out, k_out, v_out)
+
+    def _launch(self, call, check: bool = False) -> None:
+        """check: the library's own checks only, nothing is enqueued."""
+        index, batch, tokens, head, tail = call
+        if batch * tokens == 0:
+            return
+        if check:
+            tokens = 0
+        fn = load_library().kivi_rotary_apply
+        if index == self.torch._C._cuda_getDevice():
+            st = fn(*head, batch, tokens, *tail)
         else:
-            with torch.cuda.device(index):
-                st = call(self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)
+            with self.torch.cuda.device(index):
+                st = fn(*head, batch, tokens, *tail)
         _check(st, "kivi_rotary_apply")
-        return q_out, k_out, v_out
 
 
 # ---- torch-owned paged cache ---------------------------------------------------------------------
@@ -734,6 +746,10 @@ class PagedKiviCache:
                      status: bool = True) -> None:
         """Tables of a step (kivi_paged_build_tables): lens, new_tokens int32 [n], n <= num_seqs.  The new
         lengths and queue replace the old ones unless lens_out (int32 [n]) or queue_out (int64 [2]) take them."""
+        self._call(*self._tables_call(plan, plan.c, lens, new_tokens, lens_out, queue_out, stream, status))
+
+    def _tables_call(self, plan, c, lens, new_tokens, lens_out, queue_out, stream, status) -> tuple:
+        """build_tables()' checks: the arguments of _call.  c: the plan, or one of fewer tokens in its buffers."""
         self._check_plan(plan)
         i32, n = self.torch.int32, lens.shape[0] if lens.dim() == 1 else None
         _vector(self, "lens", lens, n, i32)
@@ -742,28 +758,41 @@ class PagedKiviCache:
             _vector(self, "lens_out", lens_out, n, i32)
         if queue_out is not None:
             _vector(self, "queue_out", queue_out, 2, self.torch.int64)
-        self._call(kivi_paged_build_tables, n, lens.data_ptr(), new_tokens.data_ptr(),
-                   (lens if lens_out is None else lens_out).data_ptr(),
-                   self.c.queue if queue_out is None else queue_out.data_ptr(), plan.c,
-                   self.status.data_ptr() if status else None, _raw_stream(self, stream))
+        return (kivi_paged_build_tables, n, lens.data_ptr(), new_tokens.data_ptr(),
+                (lens if lens_out is None else lens_out).data_ptr(),
+                self.c.queue if queue_out is None else queue_out.data_ptr(), c,
+                self.status.data_ptr() if status else None, _raw_stream(self, stream))
 
     def append(self, plan: PagedPlan, k, v, stream=None, status: bool = True) -> None:
         """Writes a step's tokens (kivi_paged_append): k, v fp16 [tokens][H][128] of equal strides that keep
         head rows whole, tokens at least the plan's count."""
         self._check_plan(plan)
+        call = self._append_call(plan, k, v, stream, status)
+        if call is not None:
+            self._call(*call)
+
+    def _append_call(self, plan, k, v, stream, status) -> tuple | None:
+        """append()'s checks, the library's among them: the arguments of _call, None when there are no rows."""
         shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
         _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
         _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
         if k.shape[0] == 0:
-            return
+            return None
         sk = _row_strides(k)
         if sk != _row_strides(v) or k.stride(2) != 1 or v.stride(2) != 1:
             raise ValueError(f"k, v: strides {k.stride()} and {v.stride()}; want equal strides and contiguous channels")
+        c = self._plan_of(plan, k.shape[0])
+        if (k.data_ptr() | v.data_ptr()) & 15 or (sk[0] | sk[1]) & 7:
+            raise KiviError(1, "kivi_paged_append")
+        if min(c.max_runs, c.max_tokens) * self.cfg.num_kv_heads > 0x7fffffff:
+            raise KiviError(2, "kivi_paged_append")
+        return (kivi_paged_append, c, k.data_ptr(), v.data_ptr(), sk[0], sk[1],
+                self.status.data_ptr() if status else None, _raw_stream(self, stream))
+
+    def _plan_of(self, plan, rows: int) -> kivi_paged_plan:
+        """The plan, for `rows` tokens at most: none may lie past the rows that there are."""
         c = plan.c
-        if k.shape[0] < plan.max_tokens:  # a plan of more tokens than there are rows must not read past them
-            c = kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, k.shape[0], c.max_runs)
-        self._call(kivi_paged_append, c, k.data_ptr(), v.data_ptr(), sk[0], sk[1],
-                   self.status.data_ptr() if status else None, _raw_stream(self, stream))
+        return c if rows >= plan.max_tokens else kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, rows, c.max_runs)
 
     def attend(self, lens, q, plan: PagedPlan | None = None, out=None, scale: float | None = None, window: int = 0,
                sinks: int = 0, stream=None, status: bool = True):
@@ -771,6 +800,13 @@ class PagedKiviCache:
         fp16 [rows][Hq][128].  Without a plan row i is sequence i; with one, q holds a row per new token of
         the step and only the last of each sequence is attended (other rows of out stay as they are, so
         give `out` or do not read them)."""
+        call, out = self._attend_call(lens, q, plan, out, scale, window, sinks, stream, status)
+        if q.shape[0] > 0:
+            self._call(*call)
+        return out
+
+    def _attend_call(self, lens, q, plan, out, scale, window, sinks, stream, status) -> tuple:
+        """attend()'s checks: the arguments of _call, and the output."""
         _vector(self, "lens", lens, None, self.torch.int32)
         _expect(self, "q", q, (None, None, self.cfg.head_dim), self.torch.float16)
         if plan is not None:
@@ -779,37 +815,53 @@ class PagedKiviCache:
             raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
         ws = self._workspace(q.shape[1], stream)
         out = _output(self, out, q, stream)
-        if q.shape[0] == 0:
-            return out
-        self._call(kivi_paged_decode_attention, lens.shape[0], lens.data_ptr(),
-                   None if plan is None else plan.c.cu_tokens, q.data_ptr(), q.shape[0], q.shape[1],
-                   1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
-                   _int32("sinks", sinks), out.data_ptr(), ws.ptr,
-                   ws.nbytes, self.status.data_ptr() if status else None, _raw_stream(self, stream))
-        return out
+        return (kivi_paged_decode_attention, lens.shape[0], lens.data_ptr(),
+                None if plan is None else plan.c.cu_tokens, q.data_ptr(), q.shape[0], q.shape[1],
+                1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
+                _int32("sinks", sinks), out.data_ptr(), ws.ptr,
+                ws.nbytes, self.status.data_ptr() if status else None, _raw_stream(self, stream)), out
 
     def step(self, plan: PagedPlan, lens, new_tokens, q, k, v, rotary: Rotary | None = None, q_weight=None, k_weight=None,
              eps: float = 1e-6, out=None, scale: float | None = None, window: int = 0, sinks: int = 0, stream=None,
              status: bool = True):
         """A step of a layer: tables, norms and rotation (with a rotary), append, attention; lens advances.
         q, k, v: [tokens][heads][128], fp16 (with a rotary: or bf16), packed by sequence; new_tokens sums to
-        their rows or fewer.  Returns the attention output [tokens][Hq][128] (rows: see attend)."""
+        their rows or fewer: of more, nothing is planned and KIVI_ERR_CAPACITY reported in the status word.
+        Returns the attention output [tokens][Hq][128] (rows: see attend).  A step that raises has changed
+        nothing: every argument is checked before the first launch."""
+        f16, turn = self.torch.float16, None
         if q.shape[0] > plan.max_tokens:
             raise ValueError(f"q: {q.shape[0]} rows, the plan holds {plan.max_tokens}")
-        self.build_tables(plan, lens, new_tokens, stream=stream, status=status)
         if rotary is not None:
-            q, k, v16 = rotary.apply(q, k, v if v.dtype != self.torch.float16 else None,
-                                     positions=plan.positions[:q.shape[0]], q_weight=q_weight, k_weight=k_weight, eps=eps,
-                                     stream=stream)
+            _expect(self, "q", q, (None, None, self.cfg.head_dim), q.dtype, contiguous=False)
+            turn, (q, k, v16) = rotary._arguments(q, k, v if v.dtype != f16 else None, plan.positions[:q.shape[0]], q_weight, k_weight,
+                                                  eps, None, None, None, stream)
+            rotary._launch(turn, check=True)
             v = v if v16 is None else v16
+        _expect(self, "k", k, (None, self.cfg.num_kv_heads, self.cfg.head_dim), f16, contiguous=False)
+        _expect(self, "v", v, k.shape, f16, contiguous=False)
         if _row_strides(k) != _row_strides(v) or not q.is_contiguous():
             with self.torch.cuda.stream(stream):  # None: the current stream
                 if _row_strides(k) != _row_strides(v):
-                    k, v = k.contiguous(), v.contiguous()
-                q = q.contiguous()
-        self.append(plan, k, v, stream=stream, status=status)
-        return self.attend(lens, q, plan=plan, out=out, scale=scale, window=window, sinks=sinks, stream=stream,
-                           status=status)
+                    if turn is None:
+                        k = k.contiguous()
+                    v = v.contiguous()
+                if turn is None:
+                    q = q.contiguous()
+        rows = min(q.shape[0], k.shape[0])
+        tables = self._tables_call(plan, self._plan_of(plan, max(rows, 1)), lens, new_tokens, None, None, stream, status)
+        append = self._append_call(plan, k, v, stream, status)
+        attend, out = self._attend_call(lens, q, plan, out, scale, window, sinks, stream, status)
+        if q.shape[0] > 0:
+            self._call(attend[0], 0, *attend[2:])  # of no sequences: the library's checks only
+        self._call(*tables)
+        if turn is not None:
+            rotary._launch(turn)
+        if append is not None:
+            self._call(*append)
+        if q.shape[0] > 0:
+            self._call(*attend)
+        return out
 
     def read_status(self, stream=None) -> int:
         return kivi_read_status(self.status.data_ptr(), _raw_stream(self, stream))

@@ -1,4 +1,4 @@
-"""PagedKiviCache.step as one call: steps of one token or none."""
+"""PagedKiviCache.step as one call: what it refuses changes nothing, and steps of one token or none."""
 import pytest
 
 from test_gpu_paged import _cache, _i32
@@ -9,6 +9,72 @@ torch = pytest.importorskip("torch")
 from bit_asymmetric_kv_02_b200 import kivi  # noqa: E402
 
 F16, BF16 = torch.float16, torch.bfloat16
+
+
+def _filled(**kw):
+    """A cache of two sequences of 127 and 40 tokens, with its plan, lengths and the next step's projection output."""
+    g = torch.Generator("cuda").manual_seed(1)
+    cache = _cache(num_seqs=2, num_q_heads=4, **kw)
+    plan, lens = cache.new_plan(200), _i32([0, 0])
+    x = torch.randn(167, 8, 128, generator=g, device="cuda").half()
+    cache.step(plan, lens, _i32([127, 40]), x[:, :4], x[:, 4:6], x[:, 6:])
+    return cache, plan, lens, torch.randn(2, 8, 128, generator=g, device="cuda").half()
+
+
+def _state(cache, lens):
+    names = ("block_table", "free_pages", "queue", "k_res", "v_res")
+    return [lens.clone()] + [cache.view(n).clone() for n in names]
+
+
+@pytest.mark.parametrize("rotary", [False, True])
+def test_a_refused_step_changes_nothing(rotary):
+    cache, plan, lens, x = _filled()
+    rot, new = kivi.Rotary() if rotary else None, _i32([1, 1])
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    before = _state(cache, lens)
+    odd = torch.zeros(2 * 8 * 128 + 8, dtype=F16, device="cuda")[4:4 + 2 * 8 * 128].view(2, 8, 128)  # 8 bytes off
+    wide = torch.zeros(2, 2, 130, dtype=F16, device="cuda")
+    bad = [dict(q=q.float()), dict(k=k.float()), dict(v=v.float()), dict(q=q[:, :3]), dict(k=k[:, :1]), dict(v=v[:, :1]),
+           dict(k=k[:1]), dict(v=v[:1]), dict(q=q[..., :64]), dict(k=wide[..., :128], v=wide[..., :128]), dict(q=q.cpu()),
+           dict(k=odd[:, :2], v=odd[:, 2:4]), dict(new=new.long()), dict(new=new[:1]), dict(lens=lens.long()), dict(scale=float("nan")),
+           dict(window=-1), dict(window=1 << 31), dict(sinks=-1), dict(out=torch.zeros(1, 4, 128, dtype=F16, device="cuda")),
+           dict(out=torch.zeros(2, 4, 128, device="cuda")), dict(plan=_cache(num_seqs=3).new_plan(200)),
+           dict(q=torch.zeros(2, 3, 128, dtype=F16, device="cuda")), dict(q=torch.zeros(2, 130, 128, dtype=F16, device="cuda")),
+           dict(out=torch.zeros(2 * 4 * 128 + 8, dtype=F16, device="cuda")[4:4 + 2 * 4 * 128].view(2, 4, 128))]
+    if rotary:
+        w = torch.ones(128, dtype=F16, device="cuda")
+        bad += [dict(q=q.bfloat16()), dict(k=k.bfloat16()), dict(q_weight=w.bfloat16()), dict(k_weight=w[:64]), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(q=odd[:, :4]), dict(q_weight=torch.ones(136, dtype=F16, device="cuda")[4:132])]
+    else:
+        bad += [dict(q=q.bfloat16(), k=k.bfloat16(), v=v.bfloat16()), dict(k=k.bfloat16(), v=v.bfloat16())]
+    for kw in bad:
+        args = dict(plan=plan, lens=lens, new=new, q=q, k=k, v=v)
+        args.update(kw)
+        more = {n: args.pop(n) for n in list(args) if n not in ("plan", "lens", "new", "q", "k", "v")}
+        with pytest.raises((ValueError, kivi.KiviError)):
+            cache.step(args["plan"], args["lens"], args["new"], args["q"], args["k"], args["v"], rotary=rot, **more)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(before, _state(cache, lens))), kw.keys()
+    # a number of query heads without a workspace, under capture
+    more_heads = torch.zeros(2, 8, 128, dtype=F16, device="cuda")
+    with pytest.raises(RuntimeError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            cache.step(plan, lens, new, more_heads, k, v, rotary=rot)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, _state(cache, lens)))
+    assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("rows, new", [(2, [2, 1]), (1, [1, 1]), (3, [200, 200])])
+def test_more_new_tokens_than_rows(rows, new):
+    """Nothing is planned, and the status word says so."""
+    cache, plan, lens, x = _filled()
+    x = torch.cat([x, x])[:rows]
+    before = _state(cache, lens)
+    out = torch.full((rows, 4, 128), 7.0, dtype=F16, device="cuda")
+    cache.step(plan, lens, _i32(new), x[:, :4], x[:, 4:6], x[:, 6:], out=out)
+    assert cache.read_status() == 3 and (out == 7.0).all()
+    assert all(torch.equal(a, b) for a, b in zip(before, _state(cache, lens)))
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
