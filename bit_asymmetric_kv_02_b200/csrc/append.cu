@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) paged_append_few_kerne
 
 template <int BITS, int NT>
 cudaError_t launch_tiles(const PagedAppendArgs& a, cudaStream_t stream) {
-  const int runs = a.max_runs < a.max_tokens ? a.max_runs : a.max_tokens;  // a run holds at least one new token
+  // a run holds at least one new token; without any, one block looks whether the plan says so too
+  const int runs = max(1, min(a.max_runs, a.max_tokens));
   const long long ctas = 2ll * runs * a.heads;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -283,9 +283,9 @@ int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cach
                       int32_t* dev_status, void* stream) {
   const int st = check_paged(cfg);
   if (st != KIVI_OK) return st;
-  if (!pool_ok(cache) || plan == nullptr || !aligned16(plan->runs) || !aligned16(plan->counts) || plan->max_tokens < 1 ||
-      plan->max_runs < 1 || !aligned16(k_dev) || !aligned16(v_dev) || ((token_stride | head_stride) & 7) != 0 ||
-      !status_ok(dev_status))
+  if (!pool_ok(cache) || plan == nullptr || !aligned16(plan->runs) || !aligned16(plan->counts) || plan->max_tokens < 0 ||
+      plan->max_runs < 1 || (plan->max_tokens > 0 && !(aligned16(k_dev) && aligned16(v_dev))) ||
+      ((token_stride | head_stride) & 7) != 0 || !status_ok(dev_status))
     return KIVI_ERR_INVALID_ARG;
   const long long runs = plan->max_runs < plan->max_tokens ? plan->max_runs : plan->max_tokens;
   if (runs * cfg->num_kv_heads > 0x7fffffffll) return KIVI_ERR_UNSUPPORTED;

@@ -765,21 +765,19 @@ class PagedKiviCache:
 
     def append(self, plan: PagedPlan, k, v, stream=None, status: bool = True) -> None:
         """Writes a step's tokens (kivi_paged_append): k, v fp16 [tokens][H][128] of equal strides that keep
-        head rows whole, tokens at least the plan's count."""
+        head rows whole, tokens at least the plan's count (a plan of more: KIVI_ERR_INTERNAL in the status word)."""
         self._check_plan(plan)
-        call = self._append_call(plan, k, v, stream, status)
-        if call is not None:
-            self._call(*call)
+        self._call(*self._append_call(plan, k, v, stream, status))
 
-    def _append_call(self, plan, k, v, stream, status) -> tuple | None:
-        """append()'s checks, the library's among them: the arguments of _call, None when there are no rows."""
+    def _append_call(self, plan, k, v, stream, status) -> tuple:
+        """append()'s checks, the library's among them: the arguments of _call."""
         shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
         _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
         _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
-        if k.shape[0] == 0:
-            return None
         sk = _row_strides(k)
-        if sk != _row_strides(v) or k.stride(2) != 1 or v.stride(2) != 1:
+        if k.shape[0] == 0:
+            sk = 0, 0
+        elif sk != _row_strides(v) or k.stride(2) != 1 or v.stride(2) != 1:
             raise ValueError(f"k, v: strides {k.stride()} and {v.stride()}; want equal strides and contiguous channels")
         c = self._plan_of(plan, k.shape[0])
         if (k.data_ptr() | v.data_ptr()) & 15 or (sk[0] | sk[1]) & 7:
@@ -857,8 +855,7 @@ class PagedKiviCache:
         self._call(*tables)
         if turn is not None:
             rotary._launch(turn)
-        if append is not None:
-            self._call(*append)
+        self._call(*append)
         if q.shape[0] > 0:
             self._call(*attend)
         return out

@@ -425,7 +425,8 @@ int kivi_paged_build_tables(const kivi_paged_config* cfg, const kivi_paged_cache
  * would.  k_dev, v_dev: fp16, new token t of head h at t * token_stride + h * head_stride (elements,
  * multiples of 8), tokens packed in the order of cu_tokens.  A run whose sequence, page or rows lie
  * outside the cache or max_tokens is skipped and KIVI_ERR_INTERNAL reported in dev_status, as for a plan of
- * more runs or tokens than max_runs or max_tokens, of which the first are done.  One kernel launch.
+ * more runs or tokens than max_runs or max_tokens, of which the first are done (max_tokens may be 0 here: k_dev and v_dev
+ * are not used).  One kernel launch.
  */
 int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
                       const uint16_t* k_dev, const uint16_t* v_dev, int64_t token_stride, int64_t head_stride,

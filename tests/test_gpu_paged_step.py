@@ -110,3 +110,21 @@ def test_steps_of_one_token_and_none(dtype, heads, kv):
     assert torch.equal(a.view("k_res")[1, :, 0], b.view("k_res")[1, :, 0])
     assert a.read_status() == b.read_status() == 0
     a.append(plan_a, x[:0, :kv], x[:0, kv:2 * kv].contiguous())
+
+
+def test_no_rows_for_a_plan_of_tokens():
+    """append() and step() of no rows behind tables that count some: reported, and nothing is read."""
+    cache, plan, lens, x = _filled()
+    none = x[:0, :2]
+    cache.build_tables(plan, lens, _i32([0, 0]))
+    cache.append(plan, none, none)
+    assert cache.read_status() == 0
+    residual = cache.view("k_res").clone()
+    cache.build_tables(plan, lens, _i32([1, 1]))
+    cache.append(plan, none, none)
+    assert cache.read_status() == 11 and torch.equal(cache.view("k_res"), residual)
+    cache.status.zero_()
+    cache.step(plan, lens, _i32([0, -1]), x[:0, :4], none, none)
+    assert cache.read_status() == 0 and lens.tolist() == [128, 0]
+    cache.step(plan, lens, _i32([0, 1]), x[:0, :4], none, none)
+    assert cache.read_status() == 11

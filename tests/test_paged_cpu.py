@@ -151,6 +151,14 @@ def test_attention_refusals(kivi):
     call("WORKSPACE", ws_bytes=ws - 1)
 
 
+def test_append_of_no_tokens_refusals(kivi):
+    """Without tokens the sources are not used; the rest of the rules hold."""
+    cfg, cache = _cfg(kivi), _cache(kivi)
+    for kw, st in ((dict(max_tokens=-1), 256), (dict(max_tokens=0), 252), (dict(max_tokens=0, counts=0), 256)):
+        _refused(kivi, "INVALID_ARG", kivi.kivi_paged_append, cfg, cache, _plan(kivi, **kw), 0, 0, st, 128, None, 0)
+    _refused(kivi, "INVALID_ARG", kivi.kivi_paged_append, cfg, cache, _plan(kivi, max_tokens=1), 0, FAKE, 256, 128, None, 0)
+
+
 def test_window_refusals(kivi):
     cfg = kivi.kivi_config(2, 3, 128, 2, 32, 32, 128, 1024, 0, 0)
     ws = kivi.kivi_window_workspace_bytes(cfg, 6)
