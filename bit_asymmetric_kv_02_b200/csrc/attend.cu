@@ -1614,6 +1614,10 @@ Shape shape_of(int gqa) {
   s.blocks = s.per_pass > 4 ? 2 : (gqa > 1 ? 1 : 0);
   return s;
 }
+// A workspace is the partials of any call, then the tickets: calls of other caches and numbers of query heads may use it one after
+// the other, since none of them writes partials where another one looks for its tickets, which each leaves zero.
+constexpr size_t kPartialBytes = static_cast<size_t>(kMaxCtas) * 2 * 8 * kPart * sizeof(float);
+static_assert(kPartialBytes % 256 == 0, "tickets behind the partials");
 size_t ticket_bytes(long long rows, int heads, const Shape& s) {
   return (static_cast<size_t>(rows) * heads * s.passes * s.per_pass * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
 }
@@ -1623,8 +1627,7 @@ size_t ticket_bytes(long long rows, int heads, const Shape& s) {
 size_t attend_workspace_bytes(long long rows, int heads, int gqa, long long max_units) {
   const Shape s = shape_of(gqa);
   if (rows * max_units > 0xffffffffll / (static_cast<long long>(heads) * s.passes)) return 0;
-  const size_t part = static_cast<size_t>(kMaxCtas) * 2 * (s.blocks == 0 ? 1 : 4 * s.blocks) * kPart * sizeof(float);
-  return ticket_bytes(rows, heads, s) + ((part + 255) & ~static_cast<size_t>(255));
+  return kPartialBytes + ticket_bytes(rows, heads, s);
 }
 
 cudaError_t launch_attend(AttendArgs a, int bits, void* workspace, cudaStream_t stream) {
@@ -1633,8 +1636,8 @@ cudaError_t launch_attend(AttendArgs a, int bits, void* workspace, cudaStream_t 
   a.passes = s.passes;
   a.per_pass = s.per_pass;
   a.lg_upb = a.lg_r - (bits == 2 ? 7 : 6);
-  a.tickets = static_cast<int32_t*>(workspace);
-  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(a.max_rows, a.heads, s));
+  a.partials = static_cast<float*>(workspace);
+  a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kPartialBytes);
   int dev = 0, sms = 0;
   cudaError_t e;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

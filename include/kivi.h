@@ -277,7 +277,9 @@ size_t kivi_window_workspace_bytes(const kivi_config* cfg, int32_t num_q_heads);
  * Decode attention with a sliding window and attention sinks: the query is the sequence's newest
  * token, and of the T = n_quant + n_res cached tokens it sees token t iff t < sinks or
  * t >= T - window.  Otherwise kivi_decode_attention: the same cache, layouts and workspace rules
- * (zero before its first use, left zero, not shared by overlapping calls; 256-byte aligned).  Only
+ * (zero before its first use, 256-byte aligned, not shared by overlapping calls).  The windowed and
+ * the paged call may use one workspace after one another, of any config and num_q_heads that it is
+ * large enough for; zero it again before kivi_decode_attention and the like use it, and after.  Only
  * blocks that hold a visible token are read; what the other tokens hold (NaN included) has no
  * effect, except that a block which is visible in part is dequantized with its stored (s, z).
  * window >= 0 (0: every token is visible), sinks >= 0.  Hq is any multiple of H with Hq / H <= 64.
