@@ -357,9 +357,10 @@ int decode_impl(const kivi_config* cfg, const kivi_cache* cache, const uint16_t*
   DecodePlan plan{};
   if (get_plan(cfg->bits, gqa, cfg->fine_groups, &plan) != cudaSuccess) return KIVI_ERR_CUDA;
   const size_t bh = static_cast<size_t>(cfg->batch) * cfg->num_kv_heads;
-  const size_t part_bytes = align256(static_cast<size_t>(plan.workers()) * 2 * gqa * kivi::kPartialStride * 4);
+  // tickets first: their place does not depend on num_q_heads, so calls of other numbers may use the workspace in turn
+  const size_t ticket_bytes = align256(bh * 4), part_bytes = align256(static_cast<size_t>(plan.workers()) * 2 * gqa * kivi::kPartialStride * 4);
   if (workspace_dev == nullptr || (reinterpret_cast<uintptr_t>(workspace_dev) & 255u) != 0 ||
-      workspace_bytes < part_bytes + align256(bh * 4))
+      workspace_bytes < ticket_bytes + part_bytes)
     return KIVI_ERR_WORKSPACE;
 
   DecodeArgs a{};
@@ -373,8 +374,8 @@ int decode_impl(const kivi_config* cfg, const kivi_cache* cache, const uint16_t*
   a.v_res = cache->v_res;
   a.q = q_dev;
   a.out = out_dev;
-  a.partials = static_cast<float*>(workspace_dev);
-  a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(workspace_dev) + part_bytes);
+  a.tickets = static_cast<int32_t*>(workspace_dev);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + ticket_bytes);
   a.status = dev_status;
   a.bh = static_cast<int>(bh);
   a.gqa = gqa;

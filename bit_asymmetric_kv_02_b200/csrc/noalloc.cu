@@ -60,12 +60,10 @@ extern "C" int kivi_decode_attention_noalloc(const kivi_config* cfg, const kivi_
   if (need > static_cast<size_t>(KIVI_NOALLOC_SCRATCH_BYTES)) return KIVI_ERR_WORKSPACE;
   void* base = nullptr;
   if ((st = scratch_address(&base)) != KIVI_OK) return st;
-  // The per-head tickets at the end of the scratch must be zero when the kernel starts.  The kernel
+  // The per-head tickets at the front of the scratch must be zero when the kernel starts.  The kernel
   // leaves them at zero, but a call that ended in a device error may not have: clear them.
   const size_t heads = static_cast<size_t>(cfg->batch) * static_cast<size_t>(cfg->num_kv_heads);
   const size_t ticket_bytes = (heads * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
-  if (cudaMemsetAsync(static_cast<unsigned char*>(base) + (need - ticket_bytes), 0, ticket_bytes,
-                      static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return KIVI_ERR_CUDA;
+  if (cudaMemsetAsync(base, 0, ticket_bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KIVI_ERR_CUDA;
   return kivi_decode_attention(cfg, cache, q_dev, num_q_heads, scale, out_dev, base, need, dev_status, stream);
 }

@@ -186,8 +186,9 @@ size_t kivi_decode_workspace_bytes(const kivi_config* cfg, int32_t num_q_heads);
  * Section 残差バッファ, Attention equation (scale = 1/sqrt(d_k) there; any finite scale accepted).
  * q_dev, out_dev: fp16 [B][Hq][d]; Hq must be a multiple of H.
  * workspace_dev: kivi_decode_workspace_bytes(cfg, Hq) bytes, 256-byte aligned; it must be ZERO
- * before its first use and is left zero by every call that completes without a device error
- * (after a device error, zero it again).  Calls sharing one workspace must not overlap.
+ * before its first use.  A call that completes without a device error leaves it ready for further ones of
+ * the same batch and num_kv_heads, of any Hq it is large enough for; zero it again after a device error and
+ * before calls of another cache shape or kind.  Calls sharing one workspace must not overlap.
  * dev_status: optional (may be NULL) device int32 that receives KIVI_ERR_DEVICE_TIMEOUT if a
  * bounded wait inside the kernel expires; the caller zeroes it and reads it with kivi_read_status.
  * With online_k and n_quant > 0 the residual tokens' keys are their codes (dequantized with the

@@ -54,3 +54,26 @@ def test_paged_and_windowed_calls_share_a_workspace():
     for i in order:
         kind, hq, q = calls[i]
         assert torch.equal(call(kind, hq, q, ws, buffer.numel() - 256), wants[i]), (kind, hq)
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_one_cache_with_several_numbers_of_query_heads(bits):
+    """attend() of 2, 8 and 4 query heads on one cache's workspace, heads shared between warps."""
+    g = torch.Generator("cuda").manual_seed(bits)
+    k, v = (torch.randn(1, 2, 60000, 128, generator=g, device="cuda").half() for _ in range(2))
+
+    def cache(heads):
+        c = kivi.KiviCache(1, 2, 60032, bits=bits, num_q_heads=heads)
+        c.prefill(k, v)
+        return c
+
+    qs = {h: torch.randn(1, h, 128, generator=g, device="cuda").half() for h in (2, 4, 8, 16)}
+    wants = {h: cache(h).attend(q, out=torch.full_like(q, 9.0)) for h, q in qs.items()}
+    one = cache(16)
+    for h in (16, 2, 8, 4, 16, 4, 2, 8, 16):
+        assert torch.equal(one.attend(qs[h], out=torch.full_like(qs[h], 9.0)), wants[h]), h
+    for h in (16, 2, 8):
+        out = torch.full_like(qs[h], 9.0)
+        kivi.kivi_decode_attention_noalloc(one.cfg, one.c, qs[h].data_ptr(), h, 128 ** -0.5, out.data_ptr(), None,
+                                           torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(out, wants[h]), h
