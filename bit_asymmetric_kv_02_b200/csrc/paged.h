@@ -8,6 +8,8 @@
 
 namespace kivi {
 
+constexpr int kMaxPagedSeqs = 8192;  // rows whose prefix sums one CTA keeps in shared memory
+
 struct TablesArgs {
   const int32_t* lens;
   const int32_t* new_tokens;

@@ -11,7 +11,7 @@
 namespace {
 
 constexpr int kHeadDim = 128;
-constexpr int kMaxSeqs = 8192;     // rows whose prefix sums one CTA keeps in shared memory
+using kivi::kMaxPagedSeqs;
 constexpr int kMaxGqa = 64;
 constexpr int kMaxTurnPairs = kHeadDim / 2;
 
@@ -35,7 +35,7 @@ int check_paged(const kivi_paged_config* c) {
   const int st = kivi_check_config(&one);
   if (st != KIVI_OK) return st;
   if (c->num_pages < 1 || c->num_seqs < 1 || c->max_blocks < 1) return KIVI_ERR_INVALID_ARG;
-  if (c->residual > 512 || c->num_seqs > kMaxSeqs) return KIVI_ERR_UNSUPPORTED;
+  if (c->residual > 512 || c->num_seqs > kMaxPagedSeqs) return KIVI_ERR_UNSUPPORTED;
   const long long R = c->residual;
   if (c->max_blocks * R > 0x7fffffffll || static_cast<long long>(c->num_seqs) * c->num_kv_heads * R > 0x7fffffffll ||
       static_cast<long long>(c->num_pages) * c->num_kv_heads > 0x7fffffffll)
@@ -73,7 +73,7 @@ long long max_units(int bits, int residual, long long blocks) {
 
 // Workspace of max_rows rows; 0 where the units are past the kernel's 32-bit counts.
 size_t attend_bytes(int max_rows, int heads, int num_q_heads, long long units) {
-  if (num_q_heads < 1 || num_q_heads % heads != 0 || num_q_heads / heads > kMaxGqa || max_rows > kMaxSeqs) return 0;
+  if (num_q_heads < 1 || num_q_heads % heads != 0 || num_q_heads / heads > kMaxGqa || max_rows > kMaxPagedSeqs) return 0;
   if (max_rows * units > 0x7fffffffll) return 0;
   return kivi::attend_workspace_bytes(max_rows, heads, num_q_heads / heads, units);
 }
@@ -124,7 +124,7 @@ int kivi_decode_attention_window(const kivi_config* cfg, const kivi_cache* cache
   int st = kivi_check_config(cfg);
   if (st != KIVI_OK) return st;
   if (cache == nullptr) return KIVI_ERR_INVALID_ARG;
-  if (cfg->online_k || cfg->fine_groups || cfg->batch > kMaxSeqs) return KIVI_ERR_UNSUPPORTED;
+  if (cfg->online_k || cfg->fine_groups || cfg->batch > kMaxPagedSeqs) return KIVI_ERR_UNSUPPORTED;
   const int R = cfg->residual;
   if (cache->n_quant < 0 || cache->n_quant % R != 0 || cache->n_quant > cfg->capacity || cache->n_res < 0 ||
       cache->n_res > R)

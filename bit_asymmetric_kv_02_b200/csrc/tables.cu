@@ -286,13 +286,16 @@ __global__ void __launch_bounds__(kTablesThreads) tables_kernel(const __grid_con
   }
 }
 
+constexpr size_t tables_smem(int rows) { return (6 * static_cast<size_t>(rows) + 4) * sizeof(int32_t); }
+static_assert(tables_smem(kMaxPagedSeqs) + 2 * 1024 <= 232448 - 1024, "a CTA holds 227 KB of shared memory");
+
 }  // namespace
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
-  const size_t smem = (6 * static_cast<size_t>(a.num_rows) + 4) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const size_t smem = tables_smem(a.num_rows);
+  if (smem > 48 * 1024) {  // always to the same limit: it is the function's, and another thread's call may be under way
+    const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(tables_smem(kMaxPagedSeqs)));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
