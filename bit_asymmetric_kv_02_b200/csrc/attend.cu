@@ -206,6 +206,7 @@ __device__ __forceinline__ int q_row(const AttendArgs& a, int b, bool* bad) {
     const int next = a.cu_tokens[b + 1];
     if (next == a.cu_tokens[b]) return -1;
     row = next - 1;
+    if (a.positions != nullptr && row >= 0 && row < a.max_tokens && a.positions[row] < 0) return -1;
   }
   if (row < 0 || row >= a.q_rows) {
     *bad = true;

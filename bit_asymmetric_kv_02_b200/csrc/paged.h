@@ -67,6 +67,7 @@ struct AttendArgs {
   const int32_t* block_table;  // nullptr: contiguous
   const int32_t* lens;         // nullptr: every sequence has `len` tokens, `quant` of them codes
   const int32_t* cu_tokens;    // nullptr: sequence i's query is row i
+  const int32_t* positions;    // of the step's plan, or nullptr: a negative one is of a sequence that was not served
   float* partials;
   int32_t* tickets;
   int32_t* status;
@@ -75,6 +76,7 @@ struct AttendArgs {
   int passes, per_pass;  // query passes per KV head and queries of a pass (set by launch_attend)
   int len, quant;  // without lens: tokens of every sequence, and how many of them are codes
   int q_rows;
+  int max_tokens;  // entries of positions
   int num_pages, max_blocks, blocks_per_head;
   int lg_r, lg_gk, lg_gv;
   int lg_upb;  // log2 of the units per block (set by launch_attend)

@@ -321,14 +321,16 @@ size_t kivi_paged_workspace_bytes(const kivi_paged_config* cfg, int32_t num_q_he
   return attend_bytes(cfg->num_seqs, cfg->num_kv_heads, num_q_heads, max_units(cfg->bits, cfg->residual, cfg->max_blocks));
 }
 
-int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
-                                const int32_t* lens_dev, const int32_t* cu_tokens_dev, const uint16_t* q_dev,
-                                int32_t num_q_rows, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
-                                uint16_t* out_dev, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
-                                void* stream) {
+static int paged_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
+                           const int32_t* lens_dev, const int32_t* cu_tokens_dev, const int32_t* positions_dev,
+                           int32_t max_tokens, const uint16_t* q_dev, int32_t num_q_rows, int32_t num_q_heads, float scale,
+                           int32_t window, int32_t sinks, uint16_t* out_dev, void* workspace_dev, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream) {
   int st = check_paged(cfg);
   if (st != KIVI_OK) return st;
   kivi::AttendArgs a{};
+  a.positions = positions_dev;
+  a.max_tokens = max_tokens;
   if ((st = check_attend(cfg->num_kv_heads, num_q_heads, scale, window, sinks, q_dev, out_dev, dev_status, &a)) != KIVI_OK)
     return st;
   if (!pool_ok(cache) || !aligned16(cache->block_table) || num_rows < 0 || num_rows > cfg->num_seqs || num_q_rows < 0 ||
@@ -355,6 +357,25 @@ int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_c
   a.lg_gk = log2i(cfg->group_k);
   a.lg_gv = log2i(cfg->group_v);
   return run_attend(a, cfg->bits, max_units(cfg->bits, cfg->residual, cfg->max_blocks), workspace_dev, workspace_bytes, stream);
+}
+
+int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, int32_t num_rows,
+                                const int32_t* lens_dev, const int32_t* cu_tokens_dev, const uint16_t* q_dev,
+                                int32_t num_q_rows, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                                uint16_t* out_dev, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
+                                void* stream) {
+  return paged_attention(cfg, cache, num_rows, lens_dev, cu_tokens_dev, nullptr, 0, q_dev, num_q_rows, num_q_heads, scale, window,
+                         sinks, out_dev, workspace_dev, workspace_bytes, dev_status, stream);
+}
+
+int kivi_paged_plan_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
+                              int32_t num_rows, const int32_t* lens_dev, const uint16_t* q_dev, int32_t num_q_rows,
+                              int32_t num_q_heads, float scale, int32_t window, int32_t sinks, uint16_t* out_dev,
+                              void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (plan == nullptr || !aligned16(plan->cu_tokens) || !aligned16(plan->positions) || plan->max_tokens < 1)
+    return KIVI_ERR_INVALID_ARG;
+  return paged_attention(cfg, cache, num_rows, lens_dev, plan->cu_tokens, plan->positions, plan->max_tokens, q_dev, num_q_rows,
+                         num_q_heads, scale, window, sinks, out_dev, workspace_dev, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

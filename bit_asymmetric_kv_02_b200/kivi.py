@@ -123,6 +123,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kivi_paged_append": (I32, [pcfgp, pcachep, planp, P, P, I64, I64, P, P]),
         "kivi_paged_workspace_bytes": (SZ, [pcfgp, I32]),
         "kivi_paged_decode_attention": (I32, [pcfgp, pcachep, I32, P, P, P, I32, I32, F32, I32, I32, P, P, SZ, P, P]),
+        "kivi_paged_plan_attention": (I32, [pcfgp, pcachep, planp, I32, P, P, I32, I32, F32, I32, I32, P, P, SZ, P, P]),
         "kivi_read_status": (I32, [P, P]),
         "kivi_debug_inject": (I32, [I32, U64]),
         "kivi_debug_status": (I32, []),
@@ -275,6 +276,15 @@ def kivi_paged_decode_attention(cfg, cache, num_rows: int, lens_ptr: int, cu_tok
                                                       cu_tokens_ptr, q_ptr, num_q_rows, num_q_heads, scale, window,
                                                       sinks, out_ptr, ws_ptr, ws_bytes, status_ptr, stream),
            "kivi_paged_decode_attention")
+
+
+def kivi_paged_plan_attention(cfg, cache, plan, num_rows: int, lens_ptr: int, q_ptr: int, num_q_rows: int, num_q_heads: int,
+                              scale: float, window: int, sinks: int, out_ptr: int, ws_ptr: int, ws_bytes: int,
+                              status_ptr: int | None, stream: int) -> None:
+    _check(load_library().kivi_paged_plan_attention(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(plan), num_rows,
+                                                    lens_ptr, q_ptr, num_q_rows, num_q_heads, scale, window, sinks, out_ptr,
+                                                    ws_ptr, ws_bytes, status_ptr, stream),
+           "kivi_paged_plan_attention")
 
 
 def kivi_read_status(status_ptr: int, stream: int) -> int:
@@ -795,9 +805,9 @@ class PagedKiviCache:
     def attend(self, lens, q, plan: PagedPlan | None = None, out=None, scale: float | None = None, window: int = 0,
                sinks: int = 0, stream=None, status: bool = True):
         """Attention of the newest token of each sequence (kivi_paged_decode_attention): lens int32 [n], q
-        fp16 [rows][Hq][128].  Without a plan row i is sequence i; with one, q holds a row per new token of
-        the step and only the last of each sequence is attended (other rows of out stay as they are, so
-        give `out` or do not read them)."""
+        fp16 [rows][Hq][128].  Without a plan row i is sequence i; with one (kivi_paged_plan_attention), q holds
+        a row per new token of the step, and only the last of each sequence that the tables could serve is
+        attended.  Other rows of out stay as they are: give `out` or do not read them."""
         call, out = self._attend_call(lens, q, plan, out, scale, window, sinks, stream, status)
         if q.shape[0] > 0:
             self._call(*call)
@@ -813,8 +823,9 @@ class PagedKiviCache:
             raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
         ws = self._workspace(q.shape[1], stream)
         out = _output(self, out, q, stream)
-        return (kivi_paged_decode_attention, lens.shape[0], lens.data_ptr(),
-                None if plan is None else plan.c.cu_tokens, q.data_ptr(), q.shape[0], q.shape[1],
+        rows = lens.shape[0], lens.data_ptr()
+        head = (kivi_paged_decode_attention, *rows, None) if plan is None else (kivi_paged_plan_attention, plan.c, *rows)
+        return (*head, q.data_ptr(), q.shape[0], q.shape[1],
                 1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
                 _int32("sinks", sinks), out.data_ptr(), ws.ptr,
                 ws.nbytes, self.status.data_ptr() if status else None, _raw_stream(self, stream)), out
@@ -851,7 +862,7 @@ class PagedKiviCache:
         append = self._append_call(plan, k, v, stream, status)
         attend, out = self._attend_call(lens, q, plan, out, scale, window, sinks, stream, status)
         if q.shape[0] > 0:
-            self._call(attend[0], 0, *attend[2:])  # of no sequences: the library's checks only
+            self._call(*attend[:2], 0, *attend[3:])  # of no sequences: the library's checks only
         self._call(*tables)
         if turn is not None:
             rotary._launch(turn)

@@ -446,7 +446,8 @@ size_t kivi_paged_workspace_bytes(const kivi_paged_config* cfg, int32_t num_q_he
  * lens_dev[i] tokens (the new one included), i < num_rows, with the window and sinks of
  * kivi_decode_attention_window.  q_dev, out_dev: fp16 [rows][Hq][d].  cu_tokens_dev NULL: row i is
  * sequence i.  Else (a step's cu_tokens, for batches that mix prompts and single tokens) sequence i's
- * row is cu_tokens[i + 1] - 1, its last new token, and sequences without a new token are skipped.
+ * row is cu_tokens[i + 1] - 1, its last new token, and sequences without a new token are skipped (one
+ * that the tables could not serve is not: kivi_paged_plan_attention).
  * num_q_rows: rows of q_dev and out_dev; a row outside is skipped (KIVI_ERR_INTERNAL).
  * A sequence of length 0 gives a row of zeros; a page outside the pool is left out and
  * KIVI_ERR_INTERNAL reported.  The other rows of out_dev are left as they are.
@@ -457,6 +458,16 @@ int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_c
                                 int32_t num_q_rows, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
                                 uint16_t* out_dev, void* workspace_dev, size_t workspace_bytes, int32_t* dev_status,
                                 void* stream);
+
+/*
+ * The same along a step's plan, as kivi_paged_build_tables left it: sequence i's row is that of its last
+ * new token, and sequences without a new token are skipped, as are those that the tables could not
+ * serve (positions -1): the cache does not hold their new tokens.  Their rows are left as they are.
+ */
+int kivi_paged_plan_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
+                              int32_t num_rows, const int32_t* lens_dev, const uint16_t* q_dev, int32_t num_q_rows,
+                              int32_t num_q_heads, float scale, int32_t window, int32_t sinks, uint16_t* out_dev,
+                              void* workspace_dev, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* Synchronizes `stream` and returns the device-side status word (KIVI_OK if it is 0). */
 int kivi_read_status(const int32_t* dev_status, void* stream);

@@ -128,3 +128,33 @@ def test_no_rows_for_a_plan_of_tokens():
     assert cache.read_status() == 0 and lens.tolist() == [128, 0]
     cache.step(plan, lens, _i32([0, 1]), x[:0, :4], none, none)
     assert cache.read_status() == 11
+
+
+@pytest.mark.parametrize("kind", ["no page", "too long", "not served at all"])
+def test_sequences_that_could_not_be_served(kind):
+    """Their rows of the output are left as they are: the cache does not hold their new tokens."""
+    cache, plan, lens, x = _filled(max_blocks=2)
+    new, status, served = _i32([1, 1]), 3, [False, True]
+    if kind == "no page":
+        cache.view("queue").copy_(torch.tensor([64, 64]))  # sequence 0 fills its block
+    elif kind == "too long":
+        new = _i32([1, 400])
+        x = torch.randn(401, 8, 128, generator=torch.Generator("cuda").manual_seed(2), device="cuda").half()
+        plan, served = cache.new_plan(401), [True, False]
+    else:
+        lens[0] = -5
+    rows = [0, len(x) - 1]
+    before = lens.tolist()
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    for call in ("step", "attend"):
+        out = torch.full((len(x), 4, 128), 7.0, dtype=F16, device="cuda")
+        if call == "step":
+            cache.step(plan, lens, new, q, k, v, out=out)
+            want = cache.attend(lens.clamp(min=0), q[rows].contiguous())
+        else:
+            cache.attend(lens, q.contiguous(), plan=plan, out=out)
+        assert cache.read_status() == status
+        for i in (0, 1):
+            assert torch.equal(out[rows[i]], want[i] if served[i] else torch.full_like(want[i], 7.0)), (call, i)
+            assert lens[i].item() == before[i] + (new[i].item() if served[i] else 0)
+        assert (out[1:-1] == 7.0).all()

@@ -159,6 +159,30 @@ def test_append_of_no_tokens_refusals(kivi):
     _refused(kivi, "INVALID_ARG", kivi.kivi_paged_append, cfg, cache, _plan(kivi, max_tokens=1), 0, FAKE, 256, 128, None, 0)
 
 
+def test_plan_attention_refusals(kivi):
+    cfg, cache = _cfg(kivi), _cache(kivi)
+    ws = kivi.kivi_paged_workspace_bytes(cfg, 8)
+
+    def call(code, cfg=cfg, cache=cache, rows=4, lens=FAKE, q=FAKE, q_rows=4, hq=8, scale=0.1, window=0, sinks=0, out=FAKE,
+             ws_ptr=FAKE, ws_bytes=ws, status=None, **plan):
+        _refused(kivi, code, kivi.kivi_paged_plan_attention, cfg, cache, _plan(kivi, **plan), rows, lens, q, q_rows, hq, scale,
+                 window, sinks, out, ws_ptr, ws_bytes, status, 0)
+
+    call("INVALID_ARG", cu_tokens=0)
+    call("INVALID_ARG", positions=0)
+    call("INVALID_ARG", positions=FAKE + 4)
+    call("INVALID_ARG", max_tokens=0)
+    call("INVALID_ARG", rows=5)
+    call("INVALID_ARG", lens=0)
+    call("INVALID_ARG", q_rows=-1)
+    call("INVALID_ARG", q=FAKE + 8)
+    call("INVALID_ARG", hq=3)
+    call("INVALID_ARG", scale=float("nan"))
+    call("INVALID_ARG", window=-1)
+    call("INVALID_ARG", status=FAKE + 1)
+    call("WORKSPACE", ws_bytes=ws - 1)
+
+
 def test_window_refusals(kivi):
     cfg = kivi.kivi_config(2, 3, 128, 2, 32, 32, 128, 1024, 0, 0)
     ws = kivi.kivi_window_workspace_bytes(cfg, 6)
