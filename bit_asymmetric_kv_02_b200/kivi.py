@@ -442,14 +442,14 @@ class KiviCache:
                     scale: float | None = None, stream=None, status: bool = True):
         """step() with keys and queries as the projections give them: each head normed where it has a
         weight and rotated to the new token's position (Rotary.apply), then appended and attended.
-        k_new, v_new, q: fp16 or bf16 [B][heads][128], of any strides that keep head rows whole."""
+        k_new, v_new, q: fp16 or bf16 [B][heads][128], of any strides that keep head rows whole; out fp16, as q."""
         for name, x, heads in (("q", q, None), ("k_new", k_new, self.cfg.num_kv_heads), ("v_new", v_new, self.cfg.num_kv_heads)):
             _expect(self, name, x, (self.cfg.batch, heads, self.cfg.head_dim), x.dtype, contiguous=False)
         v = None if v_new.dtype == self.torch.float16 and v_new.is_contiguous() else v_new.unsqueeze(2)
         q, k_new, v = rotary.apply(q.unsqueeze(2), k_new.unsqueeze(2), v, positions=self.n_quant + self.n_res,
                                    q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
         q, k_new, v_new = q.squeeze(2), k_new.squeeze(2), v_new if v is None else v.squeeze(2)
-        return self.step(k_new, v_new, q, out=out, scale=scale, stream=stream, status=status)
+        return self.step(k_new, v_new, q, out=_output(self, out, q, stream), scale=scale, stream=stream, status=status)
 
     def read_status(self, stream=None) -> int:
         return kivi_read_status(self.status.data_ptr(), self._stream(stream))

@@ -144,3 +144,24 @@ def test_step_rotary_of_the_contiguous_cache():
         assert (a.n_quant, a.n_res) == (b.n_quant, b.n_res) == (128, 4)
         assert torch.equal(a.view("v_res")[:, :, :4], b.view("v_res")[:, :, :4])
         assert torch.equal(a.view("k_codes")[:, :, :128], b.view("k_codes")[:, :, :128])
+
+
+def test_step_rotary_output_and_stream():
+    """A given output is checked before the cache changes; on another stream the step's own tensors are that stream's."""
+    g = torch.Generator("cuda").manual_seed(6)
+    rot = kivi.Rotary()
+    a, b = (kivi.KiviCache(2, 2, 512, num_q_heads=4) for _ in range(2))
+    x = torch.randn(2, 8, 128, generator=g, device="cuda").bfloat16()
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    for bad in (torch.zeros(2, 4, 128, device="cuda"), torch.zeros(1, 4, 128, dtype=torch.float16, device="cuda"),
+                torch.zeros(2, 8, 128, dtype=torch.float16, device="cuda")[:, ::2], torch.zeros(2, 4, 128, dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            a.step_rotary(rot, k, v, q, out=bad)
+        assert (a.n_quant, a.n_res) == (0, 0)
+    out = torch.zeros(2, 4, 128, dtype=torch.float16, device="cuda")
+    assert a.step_rotary(rot, k, v, q, out=out) is out
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = b.step_rotary(rot, k, v, q, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, out) and a.read_status() == b.read_status() == 0
