@@ -314,7 +314,7 @@ class KiviCache:
                  device=None, online_k: bool = False, fine_groups: bool = False):
         import torch
         self.torch = torch
-        self.device = torch.device(device or "cuda")
+        self.device = _device(torch, device)
         self.cfg = kivi_config(batch, num_kv_heads, head_dim, bits, group_k, group_v, residual, capacity,
                                1 if online_k else 0, 1 if fine_groups else 0)
         st = kivi_check_config(self.cfg)
@@ -489,6 +489,11 @@ def _row_strides(t) -> tuple:
 def _raw_stream(owner, stream) -> int:
     """The handle of `stream`, or of the owner's device's current stream."""
     return stream.cuda_stream if stream is not None else owner.torch._C._cuda_getCurrentRawStream(owner.index)
+
+
+def _device(torch, device):
+    """torch.device(device); None: the current CUDA device."""
+    return torch.device("cuda" if device is None else device)
 
 
 class _Same:
@@ -686,7 +691,7 @@ class PagedKiviCache:
                  tables: "PagedKiviCache | None" = None):
         import torch
         self.torch = torch
-        self.device = tables.device if tables is not None and device is None else torch.device(device or "cuda")
+        self.device = tables.device if tables is not None and device is None else _device(torch, device)
         self.cfg = kivi_paged_config(num_pages, num_seqs, max_blocks, num_kv_heads, head_dim, bits, group_k, group_v,
                                      residual)
         st = kivi_paged_check_config(self.cfg)

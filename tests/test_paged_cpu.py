@@ -282,6 +282,13 @@ def test_torch_layer_int32(kivi):
         kivi.Rotary(scaling="other")
 
 
+def test_torch_layer_device(kivi):
+    """Device 0 by its number is device 0, not whichever one is current."""
+    import torch
+    assert kivi._device(torch, 0) == torch.device("cuda", 0) == kivi._device(torch, "cuda:0")
+    assert kivi._device(torch, 1) == torch.device("cuda", 1) and kivi._device(torch, None) == torch.device("cuda")
+
+
 def test_struct_sizes(kivi):
     """The ctypes structures have the C layout of include/kivi.h."""
     assert ctypes.sizeof(kivi.kivi_rotary) == 16 + 64 * 8
