@@ -535,13 +535,10 @@ class _Workspace:
 
     def __init__(self, owner, nbytes: int, stream=None):
         torch = owner.torch
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the first call with a number of query heads allocates its workspace: make it before the capture")
-        if stream is None:
+        with torch.cuda.stream(stream):  # None: the current stream
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the first call with a number of query heads allocates its workspace: make it before the capture")
             self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=owner.device)
-        else:
-            with torch.cuda.stream(stream):
-                self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=owner.device)
         self.ptr = self.buffer.data_ptr() + (-self.buffer.data_ptr()) % 256
         self.nbytes = nbytes
 

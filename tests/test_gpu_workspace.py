@@ -77,3 +77,22 @@ def test_one_cache_with_several_numbers_of_query_heads(bits):
         kivi.kivi_decode_attention_noalloc(one.cfg, one.c, qs[h].data_ptr(), h, 128 ** -0.5, out.data_ptr(), None,
                                            torch.cuda.current_stream().cuda_stream)
         assert torch.equal(out, wants[h]), h
+
+
+def test_no_workspace_is_made_in_a_capture():
+    """Of the stream that the call runs on, which need not be the current one."""
+    cache = _cache(num_seqs=2)
+    g = torch.Generator("cuda").manual_seed(1)
+    _fill(cache, g)
+    lens, q = _i32([40, 60]), torch.randn(2, 4, 128, generator=g, device="cuda").half()
+    out, side, graph = torch.zeros_like(q), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        cache.attend(lens, q, out=out, stream=side)
+    with torch.cuda.stream(side):
+        graph.capture_end()
+    assert not cache._ws
+    cache.attend(lens, q, out=out)
+    assert out.any() and cache.read_status() == 0
