@@ -195,9 +195,13 @@ __global__ void __launch_bounds__(kRotaryThreads, 3) rotary_kernel(const __grid_
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.batch) * a.tokens;
   if (rows == 0 || a.heads == 0) return cudaSuccess;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // a warp takes all heads of a token where that fills the GPU (16 warps an SM); else the heads are shared out, down to four a
   // warp, so that a decode step's rows are all in flight at once
-  const long long want = 148ll * 16;
+  const long long want = sms * 16ll;
   long long share = (a.heads * rows + want - 1) / want;
   share = (share + kRowsAtOnce - 1) / kRowsAtOnce * kRowsAtOnce;
   if (share > a.heads) share = a.heads;
