@@ -588,7 +588,7 @@ class Rotary:
             raise ValueError(f"{name} output: expanded dimensions share memory")
         w = 0
         if weight is not None:
-            if weight.dtype is not x.dtype or weight.shape != (128,) or weight.device != x.device or not weight.is_contiguous():
+            if weight.dtype is not x.dtype or weight.shape != (128,) or weight.get_device() != x.get_device() or not weight.is_contiguous():
                 raise ValueError(f"{name} weight: want contiguous {x.dtype} [128] on {x.device}")
             w = weight.data_ptr()
         if n == 4:
@@ -603,7 +603,7 @@ class Rotary:
         positions: int32 device tensor of one entry per token ([tokens] or [B][T]), or the first position.
         Outputs may be given; an fp16 input may be its own output."""
         call, outputs = self._arguments(q, k, v, positions, q_weight, k_weight, eps, q_out, k_out, v_out, stream)
-        self._launch(call)
+        self._launch(*call)
         return outputs
 
     def _arguments(self, q, k, v, positions, q_weight, k_weight, eps, q_out, k_out, v_out, stream) -> tuple:
@@ -620,31 +620,39 @@ class Rotary:
         if v is not None:
             hv, v_out = self._heads("v", v, v_out, None, q, stream)
         batch, tokens = (q.shape[0], q.shape[2]) if n == 4 else (1, q.shape[0])
+        index = q.get_device()
         if isinstance(positions, int):
             ptr, first = None, _int32("positions", positions)
         else:
             if positions.dtype is not torch.int32 or positions.numel() != batch * tokens or not positions.is_contiguous() \
-                    or positions.device != q.device:
+                    or positions.get_device() != index:
                 raise ValueError(f"positions: want contiguous int32 of {batch * tokens} entries on {q.device}")
             ptr, first = positions.data_ptr(), 0
-        index = q.get_device()
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
-        return (index, batch, tokens, (self.c, dtype), (ptr, first, hq, hk, hv, eps, s)), (q_out, k_out, v_out)
+        return (index, batch, tokens, (self.c, dtype, batch, tokens, ptr, first, hq, hk, hv, eps, s)), (q_out, k_out, v_out)
 
-    def _launch(self, call, check: bool = False) -> None:
-        """check: the library's own checks only, nothing is enqueued."""
-        index, batch, tokens, head, tail = call
+    def _launch(self, index: int, batch: int, tokens: int, args: tuple) -> None:
         if batch * tokens == 0:
             return
-        if check:
-            tokens = 0
-        fn = load_library().kivi_rotary_apply
+        call = load_library().kivi_rotary_apply
         if index == self.torch._C._cuda_getDevice():
-            st = fn(*head, batch, tokens, *tail)
+            st = call(*args)
         else:
             with self.torch.cuda.device(index):
-                st = fn(*head, batch, tokens, *tail)
+                st = call(*args)
         _check(st, "kivi_rotary_apply")
+
+    @staticmethod
+    def _check_rules(args: tuple) -> None:
+        """The library's checks of what _arguments packed that are not made there."""
+        bad, heads = not 0.0 <= args[9] <= 3.0e38, 0
+        for packed in args[6:9]:
+            if packed is not None:
+                x, y, w, n, _, a, b, c, d, e, f = _HEADS.unpack(packed)
+                bad = bad or (x | y | w) & 15 or (a | b | c | d | e | f) & 7
+                heads += n
+        if bad or heads > 1 << 20:
+            raise KiviError(1 if bad else 2, "kivi_rotary_apply")
 
 
 # ---- torch-owned paged cache ---------------------------------------------------------------------
@@ -665,6 +673,19 @@ class PagedPlan:
         self.num_seqs, self.residual = cache.cfg.num_seqs, cache.cfg.residual
         self.c = kivi_paged_plan(self.cu_tokens.data_ptr(), self.positions.data_ptr(), self.runs.data_ptr(),
                                  self.counts.data_ptr(), max_tokens, runs)
+        self.max_runs = runs
+        self._narrow = max_tokens, self.c
+
+    def of(self, rows: int) -> kivi_paged_plan:
+        """The plan, for `rows` tokens at most: none may lie past the rows that a call has."""
+        if rows >= self.max_tokens:
+            return self.c
+        last, c = self._narrow
+        if last != rows:
+            a = self.c
+            c = kivi_paged_plan(a.cu_tokens, a.positions, a.runs, a.counts, rows, a.max_runs)
+            self._narrow = rows, c
+        return c
 
 
 class PagedKiviCache:
@@ -715,6 +736,7 @@ class PagedKiviCache:
             self.view("queue").copy_(torch.tensor([0, num_pages]))
         self.status = torch.zeros(4, dtype=torch.int32, device=self.device)
         self.index = self.status.device.index
+        self.num_seqs, self.residual, self.kv_heads, self.head_dim = num_seqs, residual, num_kv_heads, head_dim
         self._ws = {}
         if num_q_heads is not None:
             self._workspace(num_q_heads, None)
@@ -733,7 +755,7 @@ class PagedKiviCache:
             fn(self.cfg, self.c, *args)
 
     def _check_plan(self, plan: PagedPlan) -> None:
-        if plan.num_seqs != self.cfg.num_seqs or plan.residual != self.cfg.residual or plan.counts.get_device() != self.index:
+        if plan.num_seqs != self.num_seqs or plan.residual != self.residual or plan.counts.get_device() != self.index:
             raise ValueError(f"plan: of {plan.num_seqs} sequences and {plan.residual}-token blocks on {plan.counts.device}")
 
     def view(self, name: str):
@@ -782,27 +804,18 @@ class PagedKiviCache:
         self._call(*self._append_call(plan, k, v, stream, status))
 
     def _append_call(self, plan, k, v, stream, status) -> tuple:
-        """append()'s checks, the library's among them: the arguments of _call."""
-        shape = (None, self.cfg.num_kv_heads, self.cfg.head_dim)
-        _expect(self, "k", k, shape, self.torch.float16, contiguous=False)
-        _expect(self, "v", v, k.shape, self.torch.float16, contiguous=False)
-        sk = _row_strides(k)
-        if k.shape[0] == 0:
-            sk = 0, 0
-        elif sk != _row_strides(v) or k.stride(2) != 1 or v.stride(2) != 1:
-            raise ValueError(f"k, v: strides {k.stride()} and {v.stride()}; want equal strides and contiguous channels")
-        c = self._plan_of(plan, k.shape[0])
-        if (k.data_ptr() | v.data_ptr()) & 15 or (sk[0] | sk[1]) & 7:
-            raise KiviError(1, "kivi_paged_append")
-        if min(c.max_runs, c.max_tokens) * self.cfg.num_kv_heads > 0x7fffffff:
-            raise KiviError(2, "kivi_paged_append")
-        return (kivi_paged_append, c, k.data_ptr(), v.data_ptr(), sk[0], sk[1],
+        """append()'s checks: the arguments of _call."""
+        f16, shape = self.torch.float16, k.shape
+        _expect(self, "k", k, (None, self.kv_heads, self.head_dim), f16, contiguous=False)
+        if v.shape != shape or v.dtype is not f16 or v.get_device() != self.index:
+            _expect(self, "v", v, shape, f16, contiguous=False)
+        strides, other = k.stride(), v.stride()
+        if strides != other or strides[2] != 1:
+            strides = _row_strides(k)
+            if shape[0] > 0 and (strides != _row_strides(v) or k.stride(2) != 1 or other[2] != 1):
+                raise ValueError(f"k, v: strides {k.stride()} and {other}; want equal strides and contiguous channels")
+        return (kivi_paged_append, plan.of(shape[0]), k.data_ptr(), v.data_ptr(), strides[0], strides[1],
                 self.status.data_ptr() if status else None, _raw_stream(self, stream))
-
-    def _plan_of(self, plan, rows: int) -> kivi_paged_plan:
-        """The plan, for `rows` tokens at most: none may lie past the rows that there are."""
-        c = plan.c
-        return c if rows >= plan.max_tokens else kivi_paged_plan(c.cu_tokens, c.positions, c.runs, c.counts, rows, c.max_runs)
 
     def attend(self, lens, q, plan: PagedPlan | None = None, out=None, scale: float | None = None, window: int = 0,
                sinks: int = 0, stream=None, status: bool = True):
@@ -818,19 +831,20 @@ class PagedKiviCache:
     def _attend_call(self, lens, q, plan, out, scale, window, sinks, stream, status) -> tuple:
         """attend()'s checks: the arguments of _call, and the output."""
         _vector(self, "lens", lens, None, self.torch.int32)
-        _expect(self, "q", q, (None, None, self.cfg.head_dim), self.torch.float16)
+        _expect(self, "q", q, (None, None, self.head_dim), self.torch.float16)
         if plan is not None:
             self._check_plan(plan)
         elif q.shape[0] < lens.shape[0]:
             raise ValueError(f"q: {q.shape[0]} rows for {lens.shape[0]} sequences")
         ws = self._workspace(q.shape[1], stream)
         out = _output(self, out, q, stream)
-        rows = lens.shape[0], lens.data_ptr()
-        head = (kivi_paged_decode_attention, *rows, None) if plan is None else (kivi_paged_plan_attention, plan.c, *rows)
-        return (*head, q.data_ptr(), q.shape[0], q.shape[1],
-                1.0 / math.sqrt(self.cfg.head_dim) if scale is None else scale, _int32("window", window),
-                _int32("sinks", sinks), out.data_ptr(), ws.ptr,
-                ws.nbytes, self.status.data_ptr() if status else None, _raw_stream(self, stream)), out
+        n, heads, _ = q.shape
+        rest = (q.data_ptr(), n, heads, 1.0 / math.sqrt(self.head_dim) if scale is None else scale, _int32("window", window),
+                _int32("sinks", sinks), out.data_ptr(), ws.ptr, ws.nbytes, self.status.data_ptr() if status else None,
+                _raw_stream(self, stream))
+        if plan is None:
+            return (kivi_paged_decode_attention, lens.shape[0], lens.data_ptr(), None, *rest), out
+        return (kivi_paged_plan_attention, plan.c, lens.shape[0], lens.data_ptr(), *rest), out
 
     def step(self, plan: PagedPlan, lens, new_tokens, q, k, v, rotary: Rotary | None = None, q_weight=None, k_weight=None,
              eps: float = 1e-6, out=None, scale: float | None = None, window: int = 0, sinks: int = 0, stream=None,
@@ -843,34 +857,38 @@ class PagedKiviCache:
         f16, turn = self.torch.float16, None
         if q.shape[0] > plan.max_tokens:
             raise ValueError(f"q: {q.shape[0]} rows, the plan holds {plan.max_tokens}")
+        if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or q.get_device() != self.index:
+            raise ValueError(f"q, k, v: want [tokens][heads][128] on {self.status.device}, got {list(q.shape)} on {q.device}, "
+                             f"{list(k.shape)}, {list(v.shape)}")
         if rotary is not None:
-            _expect(self, "q", q, (None, None, self.cfg.head_dim), q.dtype, contiguous=False)
-            turn, (q, k, v16) = rotary._arguments(q, k, v if v.dtype != f16 else None, plan.positions[:q.shape[0]], q_weight, k_weight,
+            turn, (q, k, v16) = rotary._arguments(q, k, v if v.dtype is not f16 else None, plan.positions[:q.shape[0]], q_weight, k_weight,
                                                   eps, None, None, None, stream)
-            rotary._launch(turn, check=True)
+            rotary._check_rules(turn[3])
             v = v if v16 is None else v16
-        _expect(self, "k", k, (None, self.cfg.num_kv_heads, self.cfg.head_dim), f16, contiguous=False)
-        _expect(self, "v", v, k.shape, f16, contiguous=False)
-        if _row_strides(k) != _row_strides(v) or not q.is_contiguous():
+        apart = k.stride() != v.stride() and _row_strides(k) != _row_strides(v)
+        if apart or not q.is_contiguous():
             with self.torch.cuda.stream(stream):  # None: the current stream
-                if _row_strides(k) != _row_strides(v):
-                    if turn is None:
-                        k = k.contiguous()
-                    v = v.contiguous()
-                if turn is None:
-                    q = q.contiguous()
-        rows = min(q.shape[0], k.shape[0])
-        tables = self._tables_call(plan, self._plan_of(plan, max(rows, 1)), lens, new_tokens, None, None, stream, status)
+                if apart:
+                    k, v = k if turn is not None else k.contiguous(), v.contiguous()  # rotated keys are dense, and not there yet
+                q = q.contiguous()
         append = self._append_call(plan, k, v, stream, status)
+        rows = min(q.shape[0], k.shape[0])
+        tables = self._tables_call(plan, plan.of(max(rows, 1)), lens, new_tokens, None, None, stream, status)
         attend, out = self._attend_call(lens, q, plan, out, scale, window, sinks, stream, status)
-        if q.shape[0] > 0:
-            self._call(*attend[:2], 0, *attend[3:])  # of no sequences: the library's checks only
-        self._call(*tables)
-        if turn is not None:
-            rotary._launch(turn)
-        self._call(*append)
-        if q.shape[0] > 0:
-            self._call(*attend)
+        # the library's own checks, of calls behind the first
+        if (append[2] | append[3]) & 15 or (append[4] | append[5]) & 7:
+            raise KiviError(1, "kivi_paged_append")
+        if min(plan.max_runs, plan.max_tokens) * self.kv_heads > 0x7fffffff:
+            raise KiviError(2, "kivi_paged_append")
+        if (attend[4] | attend[10]) & 15 or window < 0 or sinks < 0 or not abs(attend[7]) <= 3.0e38:
+            raise KiviError(1, "kivi_paged_plan_attention")
+        with _on(self):
+            tables[0](self.cfg, self.c, *tables[1:])
+            if turn is not None:
+                rotary._launch(*turn)
+            append[0](self.cfg, self.c, *append[1:])
+            if q.shape[0] > 0:
+                attend[0](self.cfg, self.c, *attend[1:])
         return out
 
     def read_status(self, stream=None) -> int:
