@@ -15,6 +15,8 @@ def _filled(**kw):
     """A cache of two sequences of 127 and 40 tokens, with its plan, lengths and the next step's projection output."""
     g = torch.Generator("cuda").manual_seed(1)
     cache = _cache(num_seqs=2, num_q_heads=4, **kw)
+    for name in kivi.BUFFERS:  # rows that nobody writes are compared too, and NaN is not itself
+        cache.buffers[name].zero_()
     plan, lens = cache.new_plan(200), _i32([0, 0])
     x = torch.randn(167, 8, 128, generator=g, device="cuda").half()
     cache.step(plan, lens, _i32([127, 40]), x[:, :4], x[:, 4:6], x[:, 6:])
