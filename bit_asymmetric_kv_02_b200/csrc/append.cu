@@ -4,9 +4,9 @@
 // block in registers (quant_tiles.cuh): a block that the step completes is read once - its first rows
 // from the residual, where earlier steps left them, the others from the new tokens - and its codes and
 // (s, z) come from the same registers.  One pass over the new tokens bounds it: 4 prompts of up to 32768
-// tokens x 32 heads (1.72 GB) take 303 to 328 us by GPU, 81% to 88% of the copy bandwidth, at 4 bits 63%: its codes
+// tokens x 32 heads (1.72 GB) take 326 us, 298 on other GPUs: 82% to 89% of the copy bandwidth, at 4 bits 65%: its codes
 // take half as many instructions again, and a branch each.  A step of 64 single tokens x 32 heads,
-// 16 of which complete a block, takes 12.5 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
+// 16 of which complete a block, takes 12.3 us against 6.5 us for its bytes: the launch, the plan, a search in it and two rounds of
 // loads that depend on one another.
 // A sequence's residual holds its newest block, so the run that completes the block the residual still
 // holds part of must read those rows before the sequence's last run overwrites them: the two are
@@ -33,7 +33,7 @@ __device__ __forceinline__ Run load_run(const int32_t* runs, int r) {
 }
 
 // 64 registers a thread, so that four blocks of 128 tokens are on an SM and one's loads cover another's codes: a prompt of 4 x 32768
-// tokens x 32 heads takes 330 us, 375 with three and 483 with two (105 registers, nothing spilled).
+// tokens x 32 heads takes 300 us, 347 with three and 460 with two on the same GPU; 2 x 16000 at 4 bits 146, 172 and 231.
 constexpr int kThreadsPerSm = 1024;
 
 // Inside the cache and the source.
@@ -44,7 +44,8 @@ __device__ __forceinline__ bool run_ok(const PagedAppendArgs& a, const Run& r, i
 
 // A run that completes no block and has few rows takes a CTA for kRowHeads heads, K and V both; a longer one goes the way of the
 // blocks, a CTA per head and K or V, which has all its rows on the way at once.  More than 16 rows: 64 sequences of up to 16 new
-// tokens x 32 heads 14.3 us, 22.5 with 8 here; 6 of up to 40 x 8 heads 8.2, 12.3 with 32 here.
+// tokens x 32 heads 12.3 us, 18.0 with 8 here (R = 256: 9.1 and 33); 4 of up to 300 x 32 heads, R = 256, 7.8, 13.0 with 32 here.  What
+// loses is 100 of up to 24 x 8 heads: 8.9, 7.4 with 32 (R = 512: 27 and 7.4).
 constexpr int kFewRows = 16;
 __device__ __forceinline__ bool few_rows(const Run& r) { return r.page < 0 && r.chain == 0 && r.hi - r.lo <= kFewRows; }
 
@@ -82,7 +83,8 @@ __device__ __forceinline__ void append_rows(const PagedAppendArgs& a, const Run&
 
 // A run that completes a block, or the chain of runs that begins with it: one CTA per head and K or V.  FRESH: blocks of new tokens
 // alone, most of a prompt's, take loads without the choice of place, 150 of the 384 logic instructions a thread: 4 prompts of up to
-// 32768 tokens x 32 heads 332 -> 303 us.  A step of few tokens has next to none and is 1 us slower with the second copy of the loads.
+// 32768 tokens x 32 heads 328 -> 298 us on one GPU, 358 -> 321 on another; 4 x 6000 94 -> 84; 4 bits 2 x 16000 156 -> 147.  A step of few
+// tokens has next to none and is 0.5 us slower with the second copy of the loads.
 template <int BITS, int NT, bool FRESH>
 __device__ __forceinline__ void append_block(const PagedAppendArgs& a, Run run, int r, int num_runs, int h, bool is_v) {
   constexpr int P = 32 / BITS, R = NT / 2;
@@ -215,9 +217,10 @@ cudaError_t launch_tiles(const PagedAppendArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   // Few of the runs complete a block when there are few tokens to a run: then most of a grid of all runs x heads finds nothing to
-  // do, and a grid that fills the SMs once takes over, if that one does not.  R = 128, 32 heads, that grid against this one: 64
-  // single tokens 18.4 -> 16.4 us, 64 x up to 60 tokens 26.7 -> 22.5, 16 single tokens 10.2 -> 8.2; but 4 prompts of up to 300
-  // tokens 10.2 -> 12.3 and of up to 6000 84 -> 100, where blocks that start as others end keep the SMs fuller.
+  // do, and a grid that fills the SMs once takes over, if that one does not.  32 heads, that grid against this one: 64 single
+  // tokens 14.1 -> 12.5 us (R = 256 27.8 -> 24.2, R = 512 60.5 -> 54.3), 16 at R = 512 17.0 -> 13.5, 64 x up to 60 at R = 512 105.7 ->
+  // 79.7; but 4 prompts of up to 300 tokens 7.4 -> 9.1 and of up to 6000 84 -> 116, where blocks that start as others end keep the SMs
+  // fuller.  The rule gives 64 x up to 16 the wrong one at R = 128 (10.5 -> 12.3) and the right one at R = 256 (18.9 -> 9.1).
   const int slots = sms * (kThreadsPerSm / NT);
   if (runs <= NT && a.max_tokens < runs * (NT / 8) && ctas > slots)
     return launch_overlapped(paged_append_few_kernel<BITS, NT>, dim3(slots), NT, 0, stream, a);

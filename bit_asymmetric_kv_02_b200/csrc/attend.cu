@@ -33,11 +33,12 @@
 // What bounds it.  Read-only streams reach about the copy bandwidth here (6.46 TB/s), 1.25 us for the 8 KB of
 // every SM.  An SM issues an mma m16n8k16 every 2.0 clocks and a logic instruction for four warps every 2, and
 // beside an mma four of the latter take 2.8: with 128 products and 640 masks and shifts per 8 KB at 2 bits, the
-// instructions set the time for 2 to 4 queries (570 clocks per 8 KB, 48% of the copy bandwidth), and at
-// 4 bits, with half of either, nearly so.  One query on bytes (192 masks, 64 products) comes to 75% to 83%.
-//   64 rows of up to 8192 tokens x 32 heads, 2 bits:                162 to 178 us, by GPU (859 MB)
-//   4 rows of up to 32001 tokens x 32 heads, 4 bits:                 94 us (502 MB)
-//   16 rows of up to 32768 tokens x 8 KV heads x 4 queries, 2 bits:  66 us (204 MB)
+// instructions set the time for 2 to 4 queries (570 clocks per 8 KB, 47% of the copy bandwidth), and at
+// 4 bits, with half of either, nearly so.  One query on bytes (192 masks, 64 products) comes to 75% to 85%.
+//   64 rows of up to 8192 tokens x 32 heads, 2 bits:                177 us; 156 on other GPUs (859 MB)
+//   4 rows of up to 32001 tokens x 32 heads, 4 bits:                 95 us (502 MB)
+//   16 rows of up to 32768 tokens x 8 KV heads x 4 queries, 2 bits:  67 us (204 MB); 4 bits: 92 us (402 MB); 8 queries, 2 bits: 104 us
+//   16 rows of up to 32768 tokens x 1 KV head x 8, 32 and 64 queries, 2 bits: 27, 60 and 102 us (a pass of 8 after the other)
 // The rest is start and end: about 2 us until the ranges are known, 3.5 us for the first unit, 1.5 us to join heads in a CTA,
 // 3 us and more across CTAs.
 #include <cstdint>
@@ -61,7 +62,8 @@ constexpr float kNoMax = -1e38f;                  // reference of a part without
 constexpr float kSlack = 4.f;                     // logits may pass the reference by this much: weights up to 2^4
 
 // Warps per CTA, one CTA per SM: what registers (128, 168 and 255 a thread, next to nothing spilled) and shared memory leave room
-// for.  Fewer are slower: one query 16 warps 166 us, 12 warps 174; four queries 12 warps 74 us, 8 warps 78, 10 warps 82.
+// for.  Fewer are slower: one query 16 warps 169 us, 12 warps 186 (4 bits 93.5 and 89.9); four queries 12 warps 67 us, 10 warps 78,
+// 8 warps 72; eight queries 8 warps 104 us, 6 warps 136.
 template <int NB>
 __host__ __device__ constexpr int attend_warps() {
   return NB == 0 ? 16 : (NB == 1 ? 12 : 8);
@@ -1555,9 +1557,10 @@ __global__ void __launch_bounds__(attend_warps<NB>() * 32, 1) attend_kernel(cons
   if (split.total == 0) return;
   // Few units are spread over the SMs, but no further than pays: parts of a head that lie in one CTA join in shared memory, those of
   // several through tickets and global memory, which the last to arrive reads one after another.  A head of no more units than warps
-  // stays in a CTA, a longer one gets two CTAs' worth of SMs unless that makes it more than 20.  One sequence, 2 bits, calls in a row,
-  // against a unit per CTA: 64 tokens x 1 head 10.1 -> 8.0 us, 1024 x 4 12.5 -> 10.0, 2048 x 1 12.9 -> 11.8, 8192 x 1 19.4 -> 12.3 (with
-  // one CTA's worth 13.3), 32000 x 1 26.6 -> 15.1 (two: 15.6); what loses is 4 sequences of up to 1000 x 8: 12.0 -> 12.4.
+  // stays in a CTA, a longer one is cut into halves of a CTA unless that makes more than 20 parts.  One sequence, 2 bits, calls in a row,
+  // against a unit per CTA: 1024 tokens x 4 heads 12.7 -> 11.0 us, 2048 x 1 12.9 -> 12.2, 8192 x 1 19.9 -> 12.6 (R = 512 21.4 -> 12.7,
+  // four queries 19.8 -> 12.8), 32000 x 1 26.5 -> 15.1, 4 bits 16000 x 1 25.5 -> 14.3; what loses is 4 sequences of up to 1000 x 8:
+  // 12.0 -> 12.5, and 16 of up to 300 x 2: 11.3 -> 11.5.  Without the limit of 20: 32000 x 1 16.1, but 8192 x 1 12.1.
   split.per_cta = min(static_cast<uint32_t>(W), (split.total + gridDim.x - 1) / gridDim.x);
   if (split.per_cta < W) {
     const uint32_t per_head = (static_cast<uint32_t>(cum[T]) + active - 1) / static_cast<uint32_t>(active);

@@ -4,8 +4,9 @@
 // blocks are launched while the last one's finish, and wait there until that one is complete and its writes are visible, before
 // they touch anything.  Since every kernel lets the next one in at once, a kernel is resident while the ones before it still write:
 // nothing it reads is constant for its lifetime, so it reads by plain (or asynchronous) loads and never through the read-only
-// path (__ldg), which is not ordered behind the wait.  With it, an append captured behind tables and a rotation took the token
-// count of the step before.  One sequence of 1024 tokens x 4 heads, attention after attention: 14.4 us a call without, 12.2 us with it.
+// path (__ldg), which is not ordered behind the wait: with it, an append captured behind tables and a rotation took runs of the
+// step before.  One sequence of 1024 tokens x 4 heads, attention after attention: 12.3 us a call without the attribute, 11.0 us
+// with it; append of 64 single tokens x 32 heads 14.4 and 12.3 us.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -5,8 +5,8 @@
 // four head rows at a time: 8 lanes hold one head row (two 16-byte chunks each, chosen so that a pair's two
 // channels are in the same lane for every layout).  The token's cosines and sines are formed once, two pairs
 // a lane, and stay in registers with the norm's weights multiplied in, four factors a pair.  The rows of the
-// next four steps are on their way to shared memory meanwhile: 32768 tokens x 40 heads in bf16 take 112 to
-// 122 us by GPU, 85% to 93% of the copy bandwidth; with one step ahead in registers (24 KB in flight per SM) 141 us, and with
+// next four steps are on their way to shared memory meanwhile: 32768 tokens x 40 heads in bf16 take 120 us,
+// 108 on other GPUs, 86% to 96% of the copy bandwidth; with one step ahead in registers (24 KB in flight per SM) 141 us, and with
 // blocks of four tokens that read their cosines from shared memory for every head 145 us.
 //
 // The angle is exact: turns[i] is a pair's frequency in turns per position as a 64-bit fraction, so

@@ -9,8 +9,8 @@
 //
 // Latency bounds it: the loads of lengths and pages (0.7 us each) and the barriers of the scans.  One scan
 // takes all four sums as if every row could be served; where one cannot, a second one takes those that depend
-// on it.  Small steps take one CTA of eight warps, whose barriers are cheaper.  64 rows of one new token: 5.7 us;
-// 1000 rows of 250 to 500 new tokens: 15 us, half of them the positions (1.5 MB from eight SMs).
+// on it.  Small steps take one CTA of eight warps, whose barriers are cheaper.  64 rows of one new token in a graph: 4.7 us,
+// 6.5 with eight CTAs of 32 warps; 1000 rows of 250 to 500 new tokens: 15 us, half of them the positions (1.5 MB from eight SMs).
 #include <cstdint>
 
 #include <cooperative_groups.h>
