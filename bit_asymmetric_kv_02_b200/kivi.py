@@ -878,7 +878,7 @@ class PagedKiviCache:
         # the library's own checks, of calls behind the first
         if (append[2] | append[3]) & 15 or (append[4] | append[5]) & 7:
             raise KiviError(1, "kivi_paged_append")
-        if min(plan.max_runs, plan.max_tokens) * self.kv_heads > 0x7fffffff:
+        if min(plan.max_runs, k.shape[0]) * self.kv_heads > 0x7fffffff:
             raise KiviError(2, "kivi_paged_append")
         if (attend[4] | attend[10]) & 15 or window < 0 or sinks < 0 or not abs(attend[7]) <= 3.0e38:
             raise KiviError(1, "kivi_paged_plan_attention")
