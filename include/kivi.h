@@ -429,7 +429,8 @@ int kivi_paged_build_tables(const kivi_paged_config* cfg, const kivi_paged_cache
  * multiples of 8), tokens packed in the order of cu_tokens.  A run whose sequence, page or rows lie
  * outside the cache or max_tokens is skipped and KIVI_ERR_INTERNAL reported in dev_status, as for a plan of
  * more runs or tokens than max_runs or max_tokens, of which the first are done (max_tokens may be 0 here: k_dev and v_dev
- * are not used).  One kernel launch.
+ * are not used).  Once for each plan: the block that a run completes begins with residual rows that the
+ * call itself replaces.  One kernel launch.
  */
 int kivi_paged_append(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
                       const uint16_t* k_dev, const uint16_t* v_dev, int64_t token_stride, int64_t head_stride,
@@ -463,6 +464,7 @@ int kivi_paged_decode_attention(const kivi_paged_config* cfg, const kivi_paged_c
  * The same along a step's plan, as kivi_paged_build_tables left it: sequence i's row is that of its last
  * new token, and sequences without a new token are skipped, as are those that the tables could not
  * serve (positions -1): the cache does not hold their new tokens.  Their rows are left as they are.
+ * num_rows is at most that of the tables' call, behind which cu_tokens is of an earlier step.
  */
 int kivi_paged_plan_attention(const kivi_paged_config* cfg, const kivi_paged_cache* cache, const kivi_paged_plan* plan,
                               int32_t num_rows, const int32_t* lens_dev, const uint16_t* q_dev, int32_t num_q_rows,
